@@ -12,16 +12,19 @@ Functions (the C ABI's names without the ``mea_`` prefix):
     act_fwd, act_bwd, affine_swish_fwd, affine_swish_bwd,
     affine_act_fwd, affine_act_bwd, swish_channel_fwd, swish_channel_bwd,
     matmul_act_fwd, matmul_act_bwd,
+    norm_fwd, norm_bwd,
     concat_bn_relu_fwd, concat_bn_relu_apply, concat_bn_relu_bwd,
     act_fwd_bwd_host,
     act_bwd_workspace_bytes, affine_swish_bwd_workspace_bytes,
-    affine_act_bwd_workspace_bytes, swish_channel_bwd_workspace_bytes
+    affine_act_bwd_workspace_bytes, swish_channel_bwd_workspace_bytes,
+    norm_bwd_workspace_bytes
 Autograd / modules:
     ActivationFunction, MemoryEfficientActivation, MemoryEfficientSwish,
     AffineSwishFunction, MemoryEfficientAffineSwish,
     AffineActFunction, MemoryEfficientAffineActivation,
     SwishChannelFunction, MemoryEfficientChannelSwish,
     MLPFunction, MemoryEfficientMLP,
+    NormFunction, MemoryEfficientLayerNorm, MemoryEfficientRMSNorm,
     SharedBuffer, ConcatBNReLUConvFunction, MemoryEfficientDenseBottleneck
 """
 from __future__ import annotations
@@ -32,13 +35,15 @@ import threading
 import torch
 
 from . import _capi
-from ._capi import ACT_IDS, LAYOUT_IDS, MeaError
+from ._capi import ACT_IDS, LAYOUT_IDS, NORM_IDS, MeaError
 
 __all__ = [
     "act_fwd", "act_bwd", "act_fwd_grouped", "act_bwd_grouped", "affine_swish_fwd", "affine_swish_bwd",
     "affine_act_fwd", "affine_act_bwd", "swish_channel_fwd", "swish_channel_bwd",
     "swish_channel_fwd_grouped", "swish_channel_bwd_grouped", "swish_channel_bwd_grouped_workspace_bytes",
     "matmul_act_fwd", "matmul_act_bwd",
+    "norm_fwd", "norm_bwd", "norm_bwd_workspace_bytes",
+    "NormFunction", "MemoryEfficientLayerNorm", "MemoryEfficientRMSNorm",
     "concat_bn_relu_fwd", "concat_bn_relu_apply", "concat_bn_relu_bwd",
     "act_fwd_bwd_host",
     "act_bwd_workspace_bytes", "act_bwd_grouped_workspace_bytes", "affine_swish_bwd_workspace_bytes",
@@ -103,6 +108,18 @@ def _shaped(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
 
 def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _call(name: str, ref: torch.Tensor, *args) -> None:
+    """Calls a C entry point with ref's device current and its current stream
+    as the last argument; raises on a status other than MEA_OK."""
+    fn = getattr(_capi.lib(), name)
+    if ref.is_cuda and ref.device.index != torch.cuda.current_device():
+        with torch.cuda.device(ref.device):
+            st = fn(*args, _stream(ref))
+    else:
+        st = fn(*args, _stream(ref))
+    _capi.check(name, st)
 
 
 def _ptr(t):
@@ -553,6 +570,87 @@ def matmul_act_bwd(act: str, g: torch.Tensor, w: torch.Tensor, z: torch.Tensor, 
     return dz
 
 
+def _norm_id(norm: str) -> int:
+    try:
+        return NORM_IDS[norm]
+    except KeyError:
+        raise ValueError(f"unknown norm {norm!r}; one of {tuple(NORM_IDS)}") from None
+
+
+def _norm_args(x: torch.Tensor, params) -> tuple:
+    """Checks a normalised tensor and its per-channel parameters (None or
+    contiguous [C], all of one dtype); returns (rows, C, parameter dtype)."""
+    _need_cuda(x)
+    _dtype_id(x)
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x needs a last dimension of at least one element to normalise over")
+    C = x.shape[-1]
+    pdt = None
+    for name, t in params:
+        if t is None:
+            continue
+        _dtype_id(t)
+        _shaped(t, (C,), t.dtype if pdt is None else pdt, x.device, name)
+        pdt = t.dtype
+    return x.numel() // C, C, pdt or torch.float32
+
+
+def norm_fwd(norm: str, x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+             eps: float = 1e-5, want_stats: bool = True, out: torch.Tensor | None = None):
+    """Layer norm ("layer") or rms norm ("rms") over x's last dimension:
+    returns (y, mean, invstd), the row statistics in fp32 with x's leading
+    shape (mean None for "rms", both None without want_stats).  gamma, beta:
+    [C] in fp32 or bf16 (one dtype for both), None for 1 and 0."""
+    kind = _norm_id(norm)
+    rows, C, pdt = _norm_args(x, (("gamma", gamma), ("beta", beta)))
+    y = torch.empty_like(x) if out is None else _like(x, out, "out")
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_stats and norm == "layer" else None
+    invstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_stats else None
+    _call("mea_norm_fwd", x, kind, _dtype_id(x), _DTYPES[pdt], rows, C, x.data_ptr(), _ptr(gamma), _ptr(beta),
+          float(eps), y.data_ptr(), _ptr(mean), _ptr(invstd))
+    return y, mean, invstd
+
+
+def norm_bwd_workspace_bytes(rows: int, C: int) -> int:
+    return int(_capi.lib().mea_norm_bwd_workspace_bytes(int(rows), int(C)))
+
+
+def norm_bwd(norm: str, x: torch.Tensor, dy: torch.Tensor, gamma: torch.Tensor | None, mean: torch.Tensor | None,
+             invstd: torch.Tensor, want_dgamma: bool | None = None, want_dbeta: bool = False,
+             out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Backward of norm_fwd from x, dy and the saved statistics: returns (dx,
+    dgamma, dbeta), the parameter gradients [C] in gamma's dtype (fp32 without
+    a gamma), None where not wanted (want_dgamma: by default where gamma is
+    given).  out may be x or dy.  workspace: norm_bwd_workspace_bytes(rows, C)
+    bytes of any contents; allocated per call when not given, so that calls on
+    several streams or captured in several graphs never share one."""
+    kind = _norm_id(norm)
+    rows, C, pdt = _norm_args(x, (("gamma", gamma),))
+    if dy.dtype != x.dtype or dy.shape != x.shape:
+        raise ValueError("dy must match x in dtype and shape")
+    _like(x, dy, "dy")
+    if norm == "layer":
+        if mean is None:
+            raise ValueError("layer norm's backward needs the mean")
+        _shaped(mean, x.shape[:-1], torch.float32, x.device, "mean")
+    _shaped(invstd, x.shape[:-1], torch.float32, x.device, "invstd")
+    if want_dgamma is None:
+        want_dgamma = gamma is not None
+    dx = torch.empty_like(x) if out is None else _like(x, out, "out")
+    dgamma = torch.empty(C, dtype=pdt, device=x.device) if want_dgamma else None
+    dbeta = torch.empty(C, dtype=pdt, device=x.device) if want_dbeta else None
+    ws_ptr, ws_bytes = None, 0
+    if want_dgamma or want_dbeta:
+        if workspace is None:
+            workspace = torch.empty(norm_bwd_workspace_bytes(rows, C), dtype=torch.uint8, device=x.device)
+        _on_device(x, workspace, "workspace")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call("mea_norm_bwd", x, kind, _dtype_id(x), _DTYPES[pdt], rows, C, x.data_ptr(), dy.data_ptr(), _ptr(gamma),
+          _ptr(mean) if norm == "layer" else None, invstd.data_ptr(), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
+          ws_ptr, ws_bytes)
+    return dx, dgamma, dbeta
+
+
 def _bn_pieces(pieces):
     if not pieces:
         raise ValueError("at least one piece")
@@ -922,6 +1020,58 @@ class MemoryEfficientMLP(torch.nn.Module):
         shape = x.shape
         out = MLPFunction.apply(x.reshape(-1, shape[-1]).contiguous(), self.w1, self.w2, self.act, self.param)
         return out.view(*shape[:-1], out.shape[-1])
+
+
+class NormFunction(torch.autograd.Function):
+    """Layer or rms norm over the last dimension that keeps x and the row
+    statistics (8 bytes a row), not y or the normalised values."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, norm: str, eps: float):
+        x = x.contiguous()
+        y, mean, invstd = norm_fwd(norm, x, gamma, beta, eps)
+        ctx.norm = norm
+        ctx.save_for_backward(x, gamma, mean, invstd)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, gamma, mean, invstd = ctx.saved_tensors
+        dx, dgamma, dbeta = norm_bwd(ctx.norm, x, dy.contiguous(), gamma, mean, invstd,
+                                     want_dgamma=ctx.needs_input_grad[1], want_dbeta=ctx.needs_input_grad[2])
+        return dx, dgamma, dbeta, None, None
+
+
+class MemoryEfficientLayerNorm(torch.nn.Module):
+    """Layer norm over the last dimension (d_model elements) with learnable
+    gamma and beta (beta optional) in `dtype`; keeps its input and two floats
+    per row."""
+
+    norm = "layer"
+
+    def __init__(self, d_model: int, eps: float = 1e-5, bias: bool = True, dtype: torch.dtype = torch.float32):
+        super().__init__()
+        if dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {dtype}; use torch.float32 or torch.bfloat16")
+        self.eps = float(eps)
+        self.gamma = torch.nn.Parameter(torch.ones(d_model, dtype=dtype))
+        if bias:
+            self.beta = torch.nn.Parameter(torch.zeros(d_model, dtype=dtype))
+        else:
+            self.register_parameter("beta", None)
+
+    def forward(self, x):
+        return NormFunction.apply(x, self.gamma, self.beta, self.norm, self.eps)
+
+
+class MemoryEfficientRMSNorm(MemoryEfficientLayerNorm):
+    """Rms norm over the last dimension with a learnable gamma."""
+
+    norm = "rms"
+
+    def __init__(self, d_model: int, eps: float = 1e-5, dtype: torch.dtype = torch.float32):
+        super().__init__(d_model, eps, bias=False, dtype=dtype)
 
 
 class SharedBuffer:

@@ -1,4 +1,5 @@
-"""ctypes declarations of the C ABI in include/mea.h (libmea.so).
+"""ctypes declarations of the C ABI in include/mea.h and include/mea_block.h
+(libmea.so).
 
 Marshalling only: this module loads the shared library that sits next to it
 and declares argument and result types.  There is no fallback: if the library
@@ -11,10 +12,11 @@ import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmea.so")
 
-# Enumerations of include/mea.h.
+# Enumerations of include/mea.h and include/mea_block.h.
 MEA_RELU, MEA_LEAKY_RELU, MEA_SIGMOID, MEA_TANH, MEA_GELU_ERF, MEA_GELU_TANH, MEA_SWISH = range(7)
 MEA_F32, MEA_BF16 = 0, 1
 MEA_NCHW, MEA_NHWC = 0, 1
+MEA_LAYER_NORM, MEA_RMS_NORM = 0, 1
 MEA_OK, MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED, MEA_ERR_WORKSPACE, MEA_ERR_CUDA = range(5)
 
 ACT_IDS = {
@@ -27,6 +29,7 @@ ACT_IDS = {
     "swish": MEA_SWISH,
 }
 LAYOUT_IDS = {"nchw": MEA_NCHW, "nhwc": MEA_NHWC}
+NORM_IDS = {"layer": MEA_LAYER_NORM, "rms": MEA_RMS_NORM}
 
 # Every symbol the header declares, with (restype, argtypes).
 _vp = ctypes.c_void_p
@@ -88,6 +91,13 @@ SIGNATURES = {
     "mea_version": (_i, []),
 }
 
+# Every symbol include/mea_block.h declares.
+BLOCK_SIGNATURES = {
+    "mea_norm_fwd": (_i, [_i, _i, _i, _i64, _i64, _vp, _vp, _vp, _f, _vp, _vp, _vp, _vp]),
+    "mea_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "mea_norm_bwd": (_i, [_i, _i, _i, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+}
+
 _lib = None
 
 
@@ -108,7 +118,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing; build it with `python -m memory_efficient_activation_b200.build` "
                 "(the activation path runs only in its CUDA kernels)")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **BLOCK_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

@@ -9,10 +9,12 @@
 #include <vector>
 
 #include "../../include/mea.h"
+#include "../../include/mea_block.h"
 #include "mea_bn_api.h"
 #include "mea_channel_api.h"
 #include "mea_internal.h"
 #include "mea_matmul_api.h"
+#include "mea_norm_api.h"
 
 namespace {
 
@@ -709,6 +711,136 @@ mea_status_t mea_matmul_act_bwd(mea_act_t act, int64_t M, int64_t N, int64_t K, 
     l.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = mea::launch_matmul_act(l);
     return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul_act_bwd launch");
+}
+
+static mea_status_t check_norm(int norm, int dtype, int pdtype, int64_t rows, int64_t C)
+{
+    if (norm != MEA_LAYER_NORM && norm != MEA_RMS_NORM)
+        return fail(MEA_ERR_INVALID_ARG, "norm = %d is not a mea_norm_t", norm);
+    if (!valid_dtype(dtype)) return fail(MEA_ERR_INVALID_ARG, "dtype = %d is not a mea_dtype_t", dtype);
+    if (!valid_dtype(pdtype)) return fail(MEA_ERR_INVALID_ARG, "param_dtype = %d is not a mea_dtype_t", pdtype);
+    if (rows < 0 || C < 0) return fail(MEA_ERR_INVALID_ARG, "rows and C must be non-negative");
+    const int64_t lim = (int64_t)1 << 31;
+    if (rows >= lim || C >= lim) return fail(MEA_ERR_UNSUPPORTED, "rows and C must be below 2^31");
+    if (C > 0 && rows > kMaxElems / C) return fail(MEA_ERR_INVALID_ARG, "more than 2^60 elements");
+    return MEA_OK;
+}
+
+mea_status_t mea_norm_fwd(mea_norm_t norm, mea_dtype_t dtype, mea_dtype_t param_dtype, int64_t rows, int64_t C,
+                          const void *x, const void *gamma, const void *beta, float eps, void *y, float *mean,
+                          float *invstd, mea_stream_t stream)
+{
+    Range range_("mea_norm_fwd");
+    clear_error();
+    mea_status_t st = check_norm(norm, dtype, param_dtype, rows, C);
+    if (st != MEA_OK) return st;
+    if (!(eps >= 0.f)) return fail(MEA_ERR_INVALID_ARG, "eps must be non-negative");
+    if (rows == 0 || C == 0) return MEA_OK;
+    if (!x || !y) return fail(MEA_ERR_INVALID_ARG, "x or y is NULL");
+    if (norm == MEA_RMS_NORM) mean = nullptr;
+    const size_t bytes = (size_t)rows * C * dtype_bytes(dtype), pb = (size_t)C * dtype_bytes(param_dtype),
+                 sb = (size_t)rows * sizeof(float);
+    struct {
+        const void *p;
+        size_t n;
+    } out[3] = {{y, bytes}, {mean, sb}, {invstd, sb}}, in[3] = {{x, bytes}, {gamma, pb}, {beta, pb}};
+    for (int i = 0; i < 3; ++i) {
+        if (!out[i].p) continue;
+        for (int j = 0; j < 3; ++j) {
+            if (in[j].p && overlaps(out[i].p, out[i].n, in[j].p, in[j].n))
+                return fail(MEA_ERR_INVALID_ARG, "an output overlaps x, gamma or beta");
+            if (j < i && out[j].p && overlaps(out[i].p, out[i].n, out[j].p, out[j].n))
+                return fail(MEA_ERR_INVALID_ARG, "two outputs overlap");
+        }
+    }
+    mea::NormLaunch l{};
+    l.rms = norm == MEA_RMS_NORM;
+    l.dtype = dtype;
+    l.pdtype = param_dtype;
+    l.rows = rows;
+    l.C = C;
+    l.x = x;
+    l.gamma = gamma;
+    l.beta = beta;
+    l.eps = eps;
+    l.out = y;
+    l.mean = mean;
+    l.invstd = invstd;
+    l.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = mea::launch_norm_fwd(l);
+    return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_norm_fwd launch");
+}
+
+size_t mea_norm_bwd_workspace_bytes(int64_t rows, int64_t C)
+{
+    const int64_t lim = (int64_t)1 << 31;
+    return rows < lim && C < lim ? mea::norm_bwd_workspace_bytes(rows, C) : 0;
+}
+
+mea_status_t mea_norm_bwd(mea_norm_t norm, mea_dtype_t dtype, mea_dtype_t param_dtype, int64_t rows, int64_t C,
+                          const void *x, const void *dy, const void *gamma, const float *mean, const float *invstd,
+                          void *dx, void *dgamma, void *dbeta, void *workspace, size_t ws_bytes, mea_stream_t stream)
+{
+    Range range_("mea_norm_bwd");
+    clear_error();
+    mea_status_t st = check_norm(norm, dtype, param_dtype, rows, C);
+    if (st != MEA_OK) return st;
+    if (C == 0) return MEA_OK;
+    const size_t pb = (size_t)C * dtype_bytes(param_dtype);
+    if (rows == 0) {
+        for (void *p : {dgamma, dbeta}) {
+            if (!p) continue;
+            cudaError_t e = cudaMemsetAsync(p, 0, pb, reinterpret_cast<cudaStream_t>(stream));
+            if (e != cudaSuccess) return cuda_fail(e, "mea_norm_bwd");
+        }
+        return MEA_OK;
+    }
+    if (!x || !dy || !dx) return fail(MEA_ERR_INVALID_ARG, "x, dy or dx is NULL");
+    if (!invstd || (norm == MEA_LAYER_NORM && !mean))
+        return fail(MEA_ERR_INVALID_ARG, "the row statistics (mean, invstd) are NULL");
+    if (norm == MEA_RMS_NORM) mean = nullptr;
+    const size_t bytes = (size_t)rows * C * dtype_bytes(dtype), sb = (size_t)rows * sizeof(float);
+    if (partial_overlap(dx, x, bytes) || partial_overlap(dx, dy, bytes))
+        return fail(MEA_ERR_INVALID_ARG, "dx partially overlaps x or dy");
+    const size_t need = dgamma || dbeta ? mea::norm_bwd_workspace_bytes(rows, C) : 0;
+    if (need) {
+        if (!workspace || ws_bytes < need)
+            return fail(MEA_ERR_WORKSPACE, "workspace has %zu bytes, %zu are needed", workspace ? ws_bytes : 0, need);
+        if (reinterpret_cast<uintptr_t>(workspace) & 15u)
+            return fail(MEA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    }
+    struct {
+        const void *p;
+        size_t n;
+    } out[4] = {{dgamma, pb}, {dbeta, pb}, {need ? workspace : nullptr, need}, {dx, bytes}},
+      in[5] = {{x, bytes}, {dy, bytes}, {gamma, pb}, {mean, sb}, {invstd, sb}};
+    for (int i = 0; i < 4; ++i) {
+        if (!out[i].p) continue;
+        for (int j = 0; j < 5; ++j)
+            if (in[j].p && !(i == 3 && j < 2) && overlaps(out[i].p, out[i].n, in[j].p, in[j].n))
+                return fail(MEA_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (out[j].p && overlaps(out[i].p, out[i].n, out[j].p, out[j].n))
+                return fail(MEA_ERR_INVALID_ARG, "two of dx, dgamma, dbeta and workspace overlap");
+    }
+    mea::NormLaunch l{};
+    l.rms = norm == MEA_RMS_NORM;
+    l.dtype = dtype;
+    l.pdtype = param_dtype;
+    l.rows = rows;
+    l.C = C;
+    l.x = x;
+    l.dy = dy;
+    l.gamma = gamma;
+    l.out = dx;
+    l.mean_in = mean;
+    l.invstd_in = invstd;
+    l.dgamma = dgamma;
+    l.dbeta = dbeta;
+    l.workspace = workspace;
+    l.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = mea::launch_norm_bwd(l);
+    return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_norm_bwd launch");
 }
 
 int mea_matmul_error_word(int clear)

@@ -1,0 +1,205 @@
+"""GPU parity of the row normalisation (mea_norm_fwd, mea_norm_bwd) with its
+64-bit form; the bounds are derived in _block_ref.py."""
+import pytest
+import torch
+
+import _block_ref as ref
+import memory_efficient_activation_b200 as mea
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+NORMS = ["layer", "rms"]
+
+
+def _inputs(rows, C, dtype, pdtype, seed, shift=0.0, offset=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(n, scale=1.0, mid=0.0, dt=DT[dtype]):
+        buf = torch.empty(n + 8, dtype=dt, device="cuda")[offset:offset + n]
+        return buf.copy_(torch.randn(n, generator=gen, device="cuda") * scale + mid)
+
+    x, dy = normal(rows * C, 1.5, shift).view(rows, C), normal(rows * C).view(rows, C)
+    return x, dy, normal(C, 0.3, 1.0, DT[pdtype]), normal(C, 0.2, 0.0, DT[pdtype])
+
+
+def _check(norm, x, dy, gamma, beta, eps=1e-5):
+    y, mean, invstd = mea.norm_fwd(norm, x, gamma, beta, eps)
+    ry, rmean, rinv = ref.norm_fwd(norm, x, gamma, beta, eps)
+    by, bmean, binv = ref.norm_fwd_bounds(norm, x, gamma, beta, eps, x.dtype)
+    ref.assert_within(invstd, rinv, binv, "invstd")
+    if norm == "layer":
+        ref.assert_within(mean, rmean, bmean, "mean")
+    else:
+        assert mean is None
+    ref.assert_within(y, ry, by, "y")
+    pdt = torch.float32 if gamma is None else gamma.dtype
+    got = mea.norm_bwd(norm, x, dy, gamma, mean, invstd, want_dgamma=True, want_dbeta=True)
+    want = ref.norm_bwd(norm, x, dy, gamma, mean, invstd)
+    bounds = ref.norm_bwd_bounds(norm, x, dy, gamma, mean, invstd, x.dtype, pdt)
+    for name, g, w, b in zip(("dx", "dgamma", "dbeta"), got, want, bounds):
+        ref.assert_within(g, w, b, name)
+    return y, mean, invstd, got
+
+
+@pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("dtype,pdtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,C", [(1, 1), (3, 2), (5, 7), (1, 8), (33, 31), (2, 64), (37, 144), (9, 1001), (129, 1152),
+                                    (7, 4096), (300, 4096), (5, 4104), (3, 5001), (17, 16384), (2, 40000)])
+def test_norm_shapes(norm, dtype, pdtype, rows, C):
+    x, dy, gamma, beta = _inputs(rows, C, dtype, pdtype, rows * 31 + C)
+    _check(norm, x, dy, gamma, beta)
+
+
+@pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,C", [(40001, 8), (20000, 24), (2500, 1000), (3000, 2056), (2100, 333), (1700, 8200)])
+def test_norm_many_rows(norm, dtype, rows, C):
+    """Several slabs of column sums, uneven shares, groups of every size."""
+    x, dy, gamma, beta = _inputs(rows, C, dtype, "f32", rows + C)
+    _check(norm, x, dy, gamma, beta)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,C", [(2, 131072), (2, 131073), (1, 300001)])
+def test_norm_rows_longer_than_a_block_holds(dtype, rows, C):
+    x, dy, gamma, beta = _inputs(rows, C, dtype, "f32", C)
+    for norm in NORMS:
+        _check(norm, x, dy, gamma, beta)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_unaligned_tensors(dtype, offset):
+    x, dy, gamma, beta = _inputs(21, 272, dtype, "f32", 5, offset=offset)
+    assert x.data_ptr() % 16 or offset * x.element_size() % 16 == 0
+    _check("layer", x, dy, gamma, beta)
+
+
+@pytest.mark.parametrize("norm", NORMS)
+def test_norm_without_parameters(norm):
+    x, dy, gamma, beta = _inputs(19, 520, "bf16", "f32", 6)
+    _check(norm, x, dy, None, None)
+    _check(norm, x, dy, gamma, None)
+    _check(norm, x, dy, None, beta)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_constant_rows_and_large_offsets(dtype):
+    x, dy, gamma, beta = _inputs(12, 768, dtype, "f32", 7, shift=100.0)
+    x[3] = 0.0
+    x[4] = 2.5
+    x[5] = 1e4
+    y, mean, invstd, _ = _check("layer", x, dy, gamma, beta)
+    assert torch.equal(y[4], beta.to(y.dtype)) and abs(float(invstd[4]) - 1e-5 ** -0.5) < 1e-4 * 1e-5 ** -0.5
+    _check("rms", x, dy, gamma, beta)
+
+
+@pytest.mark.parametrize("norm", NORMS)
+def test_norm_bad_values_stay_in_their_row(norm):
+    x, dy, gamma, beta = _inputs(9, 1024, "bf16", "f32", 8)
+    clean = mea.norm_fwd(norm, x, gamma, beta)
+    dxc = mea.norm_bwd(norm, x, dy, gamma, *clean[1:])[0]
+    x[2, 5], x[6, 1000] = float("nan"), float("inf")
+    y, mean, invstd = mea.norm_fwd(norm, x, gamma, beta)
+    keep = [0, 1, 3, 4, 5, 7, 8]
+    assert torch.equal(y[keep], clean[0][keep]) and y[2].isnan().all()
+    dx = mea.norm_bwd(norm, x, dy, gamma, mean, invstd)[0]
+    assert torch.equal(dx[keep], dxc[keep]) and dx[2].isnan().all()
+
+
+def test_norm_no_rows():
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    gamma = torch.ones(64, device="cuda")
+    y, mean, invstd = mea.norm_fwd("layer", x, gamma)
+    assert y.shape == x.shape and mean.shape == (0,)
+    dx, dg, db = mea.norm_bwd("layer", x, x, gamma, mean, invstd, want_dbeta=True)
+    assert dx.shape == x.shape and not dg.any() and not db.any()
+
+
+@pytest.mark.parametrize("rows,C", [(700, 4096), (333, 1001), (2, 131072)])
+def test_norm_dx_in_place_and_deterministic(rows, C):
+    x, dy, gamma, beta = _inputs(rows, C, "bf16", "bf16", 9)
+    y, mean, invstd = mea.norm_fwd("layer", x, gamma, beta)
+    first = mea.norm_bwd("layer", x, dy, gamma, mean, invstd, want_dbeta=True)
+    for target in ("x", "dy"):
+        xc, dc = x.clone(), dy.clone()
+        got = mea.norm_bwd("layer", xc, dc, gamma, mean, invstd, want_dbeta=True, out=xc if target == "x" else dc)
+        for a, b in zip(first, got):
+            assert torch.equal(a, b)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip((y, mean, invstd), mea.norm_fwd("layer", x, gamma, beta)))
+
+
+def test_norm_writes_nothing_beyond_its_outputs():
+    rows, C = 37, 1003
+    x, dy, gamma, _ = _inputs(rows, C, "bf16", "f32", 10)
+    buf = torch.full((rows * C + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[32:32 + rows * C].view(rows, C)
+    _, mean, invstd = mea.norm_fwd("layer", x, gamma, out=out)
+    assert (buf[:32] == 7).all() and (buf[-32:] == 7).all()
+    mea.norm_bwd("layer", x, dy, gamma, mean, invstd, out=out)
+    assert (buf[:32] == 7).all() and (buf[-32:] == 7).all()
+
+
+def test_norm_on_a_side_stream_and_in_graphs():
+    """Two graphs captured on one stream and replayed on two at once: their
+    workspaces are their own."""
+    cases = [_inputs(2000, 1024, "bf16", "f32", s) for s in (11, 12)]
+    want = []
+    for x, dy, gamma, beta in cases:
+        y, mean, invstd = mea.norm_fwd("layer", x, gamma, beta)
+        want.append((y, *mea.norm_bwd("layer", x, dy, gamma, mean, invstd, want_dbeta=True)))
+    torch.cuda.synchronize()
+    side, graphs, outs = torch.cuda.Stream(), [], []
+    for x, dy, gamma, beta in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            y, mean, invstd = mea.norm_fwd("layer", x, gamma, beta)
+            outs.append((y, *mea.norm_bwd("layer", x, dy, gamma, mean, invstd, want_dbeta=True)))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, outs):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("cls,dtype", [(mea.MemoryEfficientLayerNorm, torch.float32),
+                                       (mea.MemoryEfficientRMSNorm, torch.bfloat16)])
+def test_norm_modules(cls, dtype):
+    torch.manual_seed(13)
+    m = cls(96, dtype=dtype).cuda()
+    with torch.no_grad():
+        for p in m.parameters():
+            p.add_(torch.randn_like(p) * 0.2)
+    x = torch.randn(4, 10, 96, device="cuda").bfloat16().requires_grad_()
+    xt = x.transpose(0, 1)                                  # a strided input is copied, its gradient comes back strided
+    dy = torch.randn(10, 4, 96, device="cuda").bfloat16()
+    y = m(xt)
+    y.backward(dy)
+    mean, invstd = mea.norm_fwd(cls.norm, xt.detach().contiguous(), m.gamma)[1:]
+    by = ref.norm_fwd_bounds(cls.norm, xt.detach(), m.gamma.detach(), None if m.beta is None else m.beta.detach(), 1e-5,
+                             torch.bfloat16)[0]
+    ref.assert_within(y.detach(), ref.norm_fwd(cls.norm, xt.detach(), m.gamma.detach(),
+                                               None if m.beta is None else m.beta.detach(), 1e-5)[0], by, "y")
+    want = ref.norm_bwd(cls.norm, xt.detach(), dy, m.gamma.detach(), mean, invstd)
+    b = ref.norm_bwd_bounds(cls.norm, xt.detach(), dy, m.gamma.detach(), mean, invstd, torch.bfloat16, dtype)
+    ref.assert_within(x.grad.transpose(0, 1), want[0], b[0], "dx")
+    ref.assert_within(m.gamma.grad, want[1], b[1], "dgamma")
+    assert m.gamma.grad.dtype == dtype
+    if m.beta is not None:
+        ref.assert_within(m.beta.grad, want[2], b[2], "dbeta")
+    # a frozen parameter gets none
+    m.gamma.requires_grad_(False)
+    m.zero_grad()
+    x.grad = None
+    m(x).backward(torch.ones_like(x))
+    assert m.gamma.grad is None and x.grad is not None
