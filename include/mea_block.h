@@ -1,6 +1,7 @@
 /*
  * mea_block.h -- C ABI of the transformer-block operators of libmea.so: the
- * normalisation of rows (layer norm, rms norm).
+ * normalisation of rows (layer norm, rms norm) and the gated feed-forward
+ * block (both projections, the activation and the product in one kernel).
  *
  * Everything mea.h states for its entry points holds here too: device
  * pointers owned by the caller, asynchronous calls on `stream`, status codes
@@ -9,7 +10,8 @@
  * an element count of zero is a no-op, results bitwise deterministic.
  * bf16 results are rounded once, to nearest even, from fp32 arithmetic.
  *
- * Entry points: mea_norm_fwd, mea_norm_bwd (+ _workspace_bytes).
+ * Entry points: mea_norm_fwd, mea_norm_bwd (+ _workspace_bytes);
+ * mea_matmul_gated_act_fwd, mea_matmul_gated_act_bwd.
  */
 #ifndef MEA_BLOCK_H
 #define MEA_BLOCK_H
@@ -77,6 +79,55 @@ MEA_API mea_status_t mea_norm_bwd(mea_norm_t norm, mea_dtype_t dtype, mea_dtype_
                                   int64_t C, const void *x, const void *dy, const void *gamma, const float *mean,
                                   const float *invstd, void *dx, void *dgamma, void *dbeta, void *workspace,
                                   size_t ws_bytes, mea_stream_t stream);
+
+/* Gated feed-forward block, forward: two projections of the same input, the
+ * activation of one of them and their product,
+ *   gate = X Wg^T, up = X Wu^T (bf16 inputs, fp32 accumulation on the tensor
+ *   cores), h = f(gate) up.
+ *   act, param   activation and its parameter, as in mea_act_fwd (MEA_SWISH:
+ *                SwiGLU, MEA_GELU_*: GeGLU, MEA_RELU: ReGLU, MEA_SIGMOID: GLU).
+ *   M, N, K      X is [M x K], Wg and Wu are [N x K], h is [M x N]; M or N of
+ *                0 is a no-op; K must be positive.  K and N must be multiples
+ *                of 8, each below 2^31; otherwise MEA_ERR_UNSUPPORTED.  Any M
+ *                from one token up.
+ *   x, w_gate,
+ *   w_up         device, bf16, row-major (K contiguous), read only, 16-byte
+ *                aligned (else MEA_ERR_UNSUPPORTED).  The two weights may be
+ *                the halves of one [2N x K] matrix, or the same matrix.
+ *   z            device, bf16, [M x 2N], written: row i holds gate in its
+ *                first N columns and up in its last N, rounded to bf16: the
+ *                tensor to keep for the backward.  NULL where none follows.
+ *   h            device, bf16, [M x N], written: f(gate) up formed from the
+ *                fp32 accumulators and rounded once.  NULL to form z alone; at
+ *                least one of z and h is given.  Outputs are 16-byte aligned
+ *                and overlap neither an input nor each other.
+ * Source: as mea_matmul_act_fwd (the activation in the epilogue of the matmul
+ * that feeds it), for the gated form of the block. */
+MEA_API mea_status_t mea_matmul_gated_act_fwd(mea_act_t act, int64_t M, int64_t N, int64_t K, const void *x,
+                                              const void *w_gate, const void *w_up, float param, void *z,
+                                              void *h, mea_stream_t stream);
+
+/* Gated feed-forward block, backward through the down projection out = h
+ * Wd^T and the product: with d = G Wd (never stored) and the stored z,
+ *   dz = [d up f'(gate) | d f(gate)],   h = f(gate) up.
+ * dz is the gradient of [gate | up]: dX = dz [Wg; Wu] and [dWg; dWu] = dz^T X
+ * are plain products; h, re-populated here instead of being kept by the
+ * forward, gives dWd = G^T h.
+ *   M, N, K      G is [M x K], Wd is [K x N], z and dz are [M x 2N], h is
+ *                [M x N]; restrictions as in mea_matmul_gated_act_fwd.
+ *   g            device, bf16, the gradient of out, read only.
+ *   w_down       device, bf16, row-major [K x N] (N contiguous: the weight as
+ *                the forward uses it, not transposed), read only.
+ *   z            device, bf16, [M x 2N] as the forward wrote it.
+ *   dz           device, bf16, written; may be z itself (each element is read
+ *                before it is written), no partial overlap.
+ *   h            device, bf16, written, or NULL; overlaps nothing else.
+ *   All pointers 16-byte aligned.
+ * h differs from the forward's where z's rounding moves it: it is f(gate) up
+ * of z as stored. */
+MEA_API mea_status_t mea_matmul_gated_act_bwd(mea_act_t act, int64_t M, int64_t N, int64_t K, const void *g,
+                                              const void *w_down, const void *z, float param, void *dz,
+                                              void *h, mea_stream_t stream);
 
 #ifdef __cplusplus
 }

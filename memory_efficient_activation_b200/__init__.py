@@ -11,7 +11,7 @@ stream) into those calls; PyTorch is plumbing here, not the compute path.
 Functions (the C ABI's names without the ``mea_`` prefix):
     act_fwd, act_bwd, affine_swish_fwd, affine_swish_bwd,
     affine_act_fwd, affine_act_bwd, swish_channel_fwd, swish_channel_bwd,
-    matmul_act_fwd, matmul_act_bwd,
+    matmul_act_fwd, matmul_act_bwd, matmul_gated_act_fwd, matmul_gated_act_bwd,
     norm_fwd, norm_bwd,
     concat_bn_relu_fwd, concat_bn_relu_apply, concat_bn_relu_bwd,
     act_fwd_bwd_host,
@@ -23,7 +23,7 @@ Autograd / modules:
     AffineSwishFunction, MemoryEfficientAffineSwish,
     AffineActFunction, MemoryEfficientAffineActivation,
     SwishChannelFunction, MemoryEfficientChannelSwish,
-    MLPFunction, MemoryEfficientMLP,
+    MLPFunction, MemoryEfficientMLP, GatedMLPFunction, MemoryEfficientGatedMLP,
     NormFunction, MemoryEfficientLayerNorm, MemoryEfficientRMSNorm,
     SharedBuffer, ConcatBNReLUConvFunction, MemoryEfficientDenseBottleneck
 """
@@ -41,7 +41,8 @@ __all__ = [
     "act_fwd", "act_bwd", "act_fwd_grouped", "act_bwd_grouped", "affine_swish_fwd", "affine_swish_bwd",
     "affine_act_fwd", "affine_act_bwd", "swish_channel_fwd", "swish_channel_bwd",
     "swish_channel_fwd_grouped", "swish_channel_bwd_grouped", "swish_channel_bwd_grouped_workspace_bytes",
-    "matmul_act_fwd", "matmul_act_bwd",
+    "matmul_act_fwd", "matmul_act_bwd", "matmul_gated_act_fwd", "matmul_gated_act_bwd",
+    "GatedMLPFunction", "MemoryEfficientGatedMLP",
     "norm_fwd", "norm_bwd", "norm_bwd_workspace_bytes",
     "NormFunction", "MemoryEfficientLayerNorm", "MemoryEfficientRMSNorm",
     "concat_bn_relu_fwd", "concat_bn_relu_apply", "concat_bn_relu_bwd",
@@ -570,6 +571,60 @@ def matmul_act_bwd(act: str, g: torch.Tensor, w: torch.Tensor, z: torch.Tensor, 
     return dz
 
 
+def matmul_gated_act_fwd(act: str, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, param: float = 1.0,
+                         want_z: bool = True, want_h: bool = True, z: torch.Tensor | None = None,
+                         h: torch.Tensor | None = None):
+    """Gated feed-forward block on the tensor cores, both projections and the
+    product in one kernel: gate = x w_gate^T, up = x w_up^T (x [M, K], weights
+    [N, K], bf16), h = f(gate) up.  Returns (z, h), z = [gate | up] [M, 2N] in
+    bf16 (the tensor to keep for the backward) and h [M, N]; either may be
+    skipped (None).  The weights may be the halves of one [2N, K] matrix."""
+    aid = _act_id(act)
+    for t, name in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
+        _mat2d(t, name)
+    M, K = x.shape
+    N = w_gate.shape[0]
+    if w_gate.shape[1] != K or w_up.shape != w_gate.shape:
+        raise ValueError("x, w_gate and w_up disagree in shape")
+    if w_gate.device != x.device or w_up.device != x.device:
+        raise ValueError("x, w_gate and w_up must be on the same device")
+    if want_z:
+        z = x.new_empty((M, 2 * N)) if z is None else _shaped(z, (M, 2 * N), torch.bfloat16, x.device, "z")
+    if want_h:
+        h = x.new_empty((M, N)) if h is None else _shaped(h, (M, N), torch.bfloat16, x.device, "h")
+    z, h = z if want_z else None, h if want_h else None
+    _call("mea_matmul_gated_act_fwd", x, aid, M, N, K, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+          float(param), _ptr(z), _ptr(h))
+    return z, h
+
+
+def matmul_gated_act_bwd(act: str, g: torch.Tensor, w_down: torch.Tensor, z: torch.Tensor, param: float = 1.0,
+                         want_h: bool = True, dz: torch.Tensor | None = None, h: torch.Tensor | None = None):
+    """Backward through the down projection out = h w_down^T and the gated
+    product, with g w_down never written: g [M, K] the upstream gradient,
+    w_down [K, N] as the forward uses it, z [M, 2N] the stored [gate | up].
+    Returns (dz, h): dz = [d up f'(gate) | d f(gate)] (may be written over z)
+    and h = f(gate) up re-populated for w_down's gradient (None without
+    want_h)."""
+    aid = _act_id(act)
+    for t, name in ((g, "g"), (w_down, "w_down"), (z, "z")):
+        _mat2d(t, name)
+    M, K = g.shape
+    N = w_down.shape[1]
+    if w_down.shape[0] != K or z.shape != (M, 2 * N):
+        raise ValueError("g, w_down and z disagree in shape")
+    if w_down.device != g.device or z.device != g.device:
+        raise ValueError("g, w_down and z must be on the same device")
+    dz = torch.empty_like(z) if dz is None else _shaped(dz, (M, 2 * N), torch.bfloat16, g.device, "dz")
+    if want_h:
+        h = g.new_empty((M, N)) if h is None else _shaped(h, (M, N), torch.bfloat16, g.device, "h")
+    else:
+        h = None
+    _call("mea_matmul_gated_act_bwd", g, aid, M, N, K, g.data_ptr(), w_down.data_ptr(), z.data_ptr(), float(param),
+          dz.data_ptr(), _ptr(h))
+    return dz, h
+
+
 def _norm_id(norm: str) -> int:
     try:
         return NORM_IDS[norm]
@@ -1072,6 +1127,96 @@ class MemoryEfficientRMSNorm(MemoryEfficientLayerNorm):
 
     def __init__(self, d_model: int, eps: float = 1e-5, dtype: torch.dtype = torch.float32):
         super().__init__(d_model, eps, bias=False, dtype=dtype)
+
+
+def _gated_mlp(x, w_gate_up, w_down, gamma, beta, act, param, norm, eps, keep: bool):
+    """The gated block's forward: (out, mean, invstd, z), z formed only where
+    a backward will need it."""
+    if w_gate_up.dim() != 2 or w_gate_up.shape[0] % 2:
+        raise ValueError("w_gate_up must be [2 d_hidden, d_model]")
+    H = w_gate_up.shape[0] // 2
+    n, mean, invstd = (x, None, None) if norm is None else norm_fwd(norm, x, gamma, beta, eps, want_stats=keep)
+    z, h = matmul_gated_act_fwd(act, n, w_gate_up[:H], w_gate_up[H:], param, want_z=keep)
+    return torch.matmul(h, w_down.t()), mean, invstd, z
+
+
+class GatedMLPFunction(torch.autograd.Function):
+    """out = (f(n Wg^T) * (n Wu^T)) Wd^T, n = x or its layer or rms norm, that
+    keeps x, the row statistics and z = [gate | up] (bf16) for the backward:
+    neither n nor the product h.  The forward's two projections, activation
+    and product are one kernel; the backward multiplies dout Wd by the
+    product's derivatives inside the matmul that forms it, in which h is
+    re-populated, and forms n again from x.  The other products (h Wd^T;
+    dWd = dout^T h, d[Wg; Wu] = dz^T n, dn = dz [Wg; Wu]) are plain matmuls
+    (torch.matmul).  w_gate_up [2 d_hidden, d_model] holds Wg above Wu."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate_up, w_down, gamma, beta, act: str, param: float, norm: str | None, eps: float):
+        x = x.contiguous()
+        out, mean, invstd, z = _gated_mlp(x, w_gate_up, w_down, gamma, beta, act, param, norm, eps, True)
+        ctx.args = (act, param, norm, eps)
+        ctx.save_for_backward(x, w_gate_up, w_down, gamma, beta, mean, invstd, z)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, w_gate_up, w_down, gamma, beta, mean, invstd, z = ctx.saved_tensors
+        act, param, norm, eps = ctx.args
+        need = ctx.needs_input_grad
+        dout = dout.contiguous()
+        dz, h = matmul_gated_act_bwd(act, dout, w_down, z, param, want_h=need[2])
+        dw_down = torch.matmul(dout.t(), h) if need[2] else None
+        del h
+        dw1 = None
+        if need[1]:
+            n = x if norm is None else norm_fwd(norm, x, gamma, beta, eps, want_stats=False)[0]
+            dw1 = torch.matmul(dz.t(), n)
+            del n
+        dx = dgamma = dbeta = None
+        if need[0] or need[3] or need[4]:
+            dx = torch.matmul(dz, w_gate_up)
+            if norm is not None:
+                dx, dgamma, dbeta = norm_bwd(norm, x, dx, gamma, mean, invstd, want_dgamma=need[3], want_dbeta=need[4],
+                                             out=dx)
+        return dx, dw1, dw_down, dgamma, dbeta, None, None, None, None
+
+
+class MemoryEfficientGatedMLP(torch.nn.Module):
+    """Gated feed-forward block in bf16, no biases: the gate and up
+    projections (d_model -> d_hidden, one [2 d_hidden, d_model] parameter), f
+    of the gate times up, and the down projection, after an optional norm
+    ("layer" or "rms") of the input.  Keeps the input, its row statistics and
+    the two pre-activations for the backward.  d_model and d_hidden must be
+    multiples of 8; inputs are [..., d_model] bf16 CUDA tensors."""
+
+    def __init__(self, d_model: int, d_hidden: int, act: str = "swish", param: float | None = None,
+                 norm: str | None = None, eps: float = 1e-5):
+        super().__init__()
+        _act_id(act)
+        if norm is not None:
+            _norm_id(norm)
+        if d_model % 8 or d_hidden % 8:
+            raise ValueError("d_model and d_hidden must be multiples of 8")
+        self.act, self.norm, self.eps = act, norm, float(eps)
+        self.param = (0.01 if act == "leaky_relu" else 1.0) if param is None else float(param)
+        self.w_gate_up = torch.nn.Parameter(torch.empty(2 * d_hidden, d_model, dtype=torch.bfloat16))
+        self.w_down = torch.nn.Parameter(torch.empty(d_model, d_hidden, dtype=torch.bfloat16))
+        for name, make, has in (("gamma", torch.ones, norm is not None), ("beta", torch.zeros, norm == "layer")):
+            self.register_parameter(name, torch.nn.Parameter(make(d_model, dtype=torch.bfloat16)) if has else None)
+        with torch.no_grad():
+            self.w_gate_up.normal_(0.0, d_model ** -0.5)
+            self.w_down.normal_(0.0, d_hidden ** -0.5)
+
+    def forward(self, x):
+        shape = x.shape
+        x = x.reshape(-1, shape[-1])
+        args = (self.w_gate_up, self.w_down, self.gamma, self.beta, self.act, self.param, self.norm, self.eps)
+        if torch.is_grad_enabled():
+            out = GatedMLPFunction.apply(x, *args)
+        else:
+            out = _gated_mlp(x.contiguous(), *args, False)[0]
+        return out.view(*shape[:-1], out.shape[-1])
 
 
 class SharedBuffer:

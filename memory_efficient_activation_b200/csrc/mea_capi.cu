@@ -12,6 +12,7 @@
 #include "../../include/mea_block.h"
 #include "mea_bn_api.h"
 #include "mea_channel_api.h"
+#include "mea_gated_api.h"
 #include "mea_internal.h"
 #include "mea_matmul_api.h"
 #include "mea_norm_api.h"
@@ -713,6 +714,92 @@ mea_status_t mea_matmul_act_bwd(mea_act_t act, int64_t M, int64_t N, int64_t K, 
     return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul_act_bwd launch");
 }
 
+// M, N and K of a gated product; *done is set where there is nothing to do.
+static mea_status_t check_gated(int act, int64_t M, int64_t N, int64_t K, bool *done)
+{
+    mea_status_t st = check_matmul("", act, M, N, K);
+    *done = st == MEA_OK && (M == 0 || N == 0);
+    if (st != MEA_OK || *done) return st;
+    if (K == 0) return fail(MEA_ERR_UNSUPPORTED, "K = 0 (an empty product) is not served");
+    if (K % 8 || N % 8) return fail(MEA_ERR_UNSUPPORTED, "K and N must be multiples of 8");
+    return MEA_OK;
+}
+
+mea_status_t mea_matmul_gated_act_fwd(mea_act_t act, int64_t M, int64_t N, int64_t K, const void *x,
+                                      const void *w_gate, const void *w_up, float param, void *z, void *h,
+                                      mea_stream_t stream)
+{
+    Range range_("mea_matmul_gated_act_fwd");
+    clear_error();
+    bool done;
+    mea_status_t st = check_gated(act, M, N, K, &done);
+    if (st != MEA_OK || done) return st;
+    if (!x || !w_gate || !w_up) return fail(MEA_ERR_INVALID_ARG, "x, w_gate or w_up is NULL");
+    if (!z && !h) return fail(MEA_ERR_INVALID_ARG, "z and h are both NULL");
+    for (const void *p : {x, w_gate, w_up, (const void *)z, (const void *)h})
+        if (!aligned16(p)) return fail(MEA_ERR_UNSUPPORTED, "x, w_gate, w_up, z and h must be 16-byte aligned");
+    const size_t bx = (size_t)M * K * 2, bw = (size_t)N * K * 2, bh = (size_t)M * N * 2;
+    const struct {
+        void *p;
+        size_t n;
+    } out[2] = {{z, 2 * bh}, {h, bh}};
+    for (const auto &o : out)
+        if (o.p && (overlaps(o.p, o.n, x, bx) || overlaps(o.p, o.n, w_gate, bw) || overlaps(o.p, o.n, w_up, bw)))
+            return fail(MEA_ERR_INVALID_ARG, "an output overlaps x, w_gate or w_up");
+    if (z && h && overlaps(z, 2 * bh, h, bh)) return fail(MEA_ERR_INVALID_ARG, "z overlaps h");
+    mea::GatedLaunch l{};
+    l.act = act;
+    l.mode = 0;
+    l.M = M;
+    l.N = N;
+    l.K = K;
+    l.x = x;
+    l.w0 = w_gate;
+    l.w1 = w_up;
+    l.z = z;
+    l.h = h;
+    l.param = param;
+    l.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = mea::launch_gated(l);
+    return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul_gated_act_fwd launch");
+}
+
+mea_status_t mea_matmul_gated_act_bwd(mea_act_t act, int64_t M, int64_t N, int64_t K, const void *g,
+                                      const void *w_down, const void *z, float param, void *dz, void *h,
+                                      mea_stream_t stream)
+{
+    Range range_("mea_matmul_gated_act_bwd");
+    clear_error();
+    bool done;
+    mea_status_t st = check_gated(act, M, N, K, &done);
+    if (st != MEA_OK || done) return st;
+    if (!g || !w_down || !z || !dz) return fail(MEA_ERR_INVALID_ARG, "g, w_down, z or dz is NULL");
+    for (const void *p : {g, w_down, z, (const void *)dz, (const void *)h})
+        if (!aligned16(p)) return fail(MEA_ERR_UNSUPPORTED, "g, w_down, z, dz and h must be 16-byte aligned");
+    const size_t bg = (size_t)M * K * 2, bw = (size_t)N * K * 2, bh = (size_t)M * N * 2;
+    if (overlaps(dz, 2 * bh, g, bg) || overlaps(dz, 2 * bh, w_down, bw))
+        return fail(MEA_ERR_INVALID_ARG, "dz overlaps g or w_down");
+    if (partial_overlap(dz, z, 2 * bh)) return fail(MEA_ERR_INVALID_ARG, "dz partially overlaps z");
+    if (h && (overlaps(h, bh, g, bg) || overlaps(h, bh, w_down, bw) || overlaps(h, bh, z, 2 * bh) ||
+              overlaps(h, bh, dz, 2 * bh)))
+        return fail(MEA_ERR_INVALID_ARG, "h overlaps g, w_down, z or dz");
+    mea::GatedLaunch l{};
+    l.act = act;
+    l.mode = 1;
+    l.M = M;
+    l.N = N;
+    l.K = K;
+    l.x = g;
+    l.w0 = w_down;
+    l.zin = z;
+    l.z = dz;
+    l.h = h;
+    l.param = param;
+    l.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = mea::launch_gated(l);
+    return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul_gated_act_bwd launch");
+}
+
 static mea_status_t check_norm(int norm, int dtype, int pdtype, int64_t rows, int64_t C)
 {
     if (norm != MEA_LAYER_NORM && norm != MEA_RMS_NORM)
@@ -846,13 +933,14 @@ mea_status_t mea_norm_bwd(mea_norm_t norm, mea_dtype_t dtype, mea_dtype_t param_
 int mea_matmul_error_word(int clear)
 {
     clear_error();
-    unsigned int w = 0;
+    unsigned int w = 0, wg = 0;
     cudaError_t e = mea::matmul_error_word(clear, &w);
+    if (e == cudaSuccess) e = mea::gated_error_word(clear, &wg);
     if (e != cudaSuccess) {
         cuda_fail(e, "mea_matmul_error_word");
         return -1;
     }
-    return (int)w;
+    return (int)(w | wg);
 }
 
 static mea_status_t bn_common(const char *name, int dtype, int npieces, const void *const *pieces,

@@ -1,0 +1,35 @@
+// mea_gated_api.h -- host-side interface of the gated feed-forward kernels
+// (both projections, the activation and the product on the tensor cores).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace mea {
+
+// All matrices are row-major bf16.
+//   mode 0 (forward):  gate = X Wg^T, up = X Wu^T with X [M x K], Wg, Wu
+//                      [N x K]; z [M x 2N] = [gate | up] (nullable), h [M x N]
+//                      = f(gate) up (nullable; at least one of the two).
+//   mode 1 (backward): d = G Wd with G = x [M x K], Wd = w0 [K x N]; zin the
+//                      stored [M x 2N]; z [M x 2N] = [d up f'(gate) | d
+//                      f(gate)], h (nullable) = f(gate) up.
+struct GatedLaunch {
+    int act;
+    int mode;
+    int64_t M, N, K;
+    const void *x;
+    const void *w0;
+    const void *w1;      // forward only
+    const void *zin;     // backward only
+    void *z;
+    void *h;
+    float param;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_gated(const GatedLaunch &a);
+cudaError_t gated_error_word(int clear, unsigned int *word);   // synchronous
+
+}  // namespace mea

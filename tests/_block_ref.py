@@ -140,3 +140,56 @@ def assert_within(got, ref, bound, what):
         i = tuple(int(v) for v in bad.nonzero()[0])
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {i}: {float(got[i])} for "
                              f"{float(ref[i])}, error {float(err[i]):.3g} over {float(bound[i]):.3g}")
+
+
+# |f'| never exceeds this (sigmoid's quarter, the GELUs' and Swish's overshoot)
+LIPSCHITZ = {"relu": 1.0, "leaky_relu": 1.0, "sigmoid": 0.25, "tanh": 1.0, "gelu_erf": 1.1290, "gelu_tanh": 1.1290,
+             "swish": 1.0999}
+# f and f' as the bf16 kernels evaluate them: tanh.approx is good to 2^-11, every other form to better than 2^-12;
+# next to a zero of f' (whose terms cancel) an absolute 2^-20 on top.
+F_REL, DF_ABS = 2.0 ** -11, 2.0 ** -20
+
+
+def _acc(x, w, K):
+    """Bound on an fp32 accumulation over k in any order: K additions, each off
+    by at most a step of a partial sum below S = sum |x w|."""
+    return K * 2.0 ** -23 * (x.double().abs() @ w.double().abs())
+
+
+def gated_fwd_bounds(name, x, w_gate, w_up, param=1.0):
+    """Bounds on z = [gate | up] and h: the accumulations' errors carried
+    through f (Lipschitz) and the product, f's evaluation, one rounding."""
+    K = x.shape[1]
+    gate, up, h = gated_fwd(name, x, w_gate, w_up, param)
+    eg, eu = _acc(x, w_gate.t(), K), _acc(x, w_up.t(), K)
+    f = act(name, gate, param)[0].abs()
+    ef = LIPSCHITZ[name] * eg + F_REL * f
+    eh = ef * (up.abs() + eu) + f * eu + 2 * U32 * h.abs()
+    half = HALF[torch.bfloat16]
+    z, ez = torch.cat([gate, up], 1).abs(), torch.cat([eg, eu], 1)
+    return ez + half * (z + ez) + TINY, eh + half * (h.abs() + eh) + TINY * (1 + up.abs())
+
+
+def gated_bwd_bounds(name, g, w_down, z, param=1.0):
+    """Bounds on dz and h for a z taken as given."""
+    N, K = w_down.shape[1], g.shape[1]
+    gate, up = z.double()[:, :N], z.double()[:, N:].abs()
+    ed = _acc(g, w_down, K)
+    d = (g.double() @ w_down.double()).abs()
+    f, df = (v.abs() for v in act(name, gate, param))
+    eg = ed * up * df + (d + ed) * up * (F_REL * df + DF_ABS)
+    eu = ed * f + (d + ed) * F_REL * f
+    ref, h = gated_bwd(name, g, w_down, z, param)
+    half = HALF[torch.bfloat16]
+    e = torch.cat([eg, eu], 1)
+    eh = F_REL * h.abs()
+    return (e + half * (ref.abs() + e) + TINY * (1 + torch.cat([d * up, d], 1)),
+            eh + half * (h.abs() + eh) + TINY * (1 + up))
+
+
+def assert_close_overall(got, ref, what, parts=1):
+    """Norm of the error at most half a bf16 step of the norm of the result
+    (the rms of a rounding is below half a step), times `parts` roundings: a
+    fault in the order of operands or of K steps breaks every element."""
+    err, norm = float((got.double() - ref).norm()), float(ref.norm())
+    assert err <= parts * HALF[torch.bfloat16] * norm + TINY, (what, err / max(norm, TINY))
