@@ -11,7 +11,7 @@
  * bf16 results are rounded once, to nearest even, from fp32 arithmetic.
  *
  * Entry points: mea_norm_fwd, mea_norm_bwd (+ _workspace_bytes);
- * mea_matmul_gated_act_fwd, mea_matmul_gated_act_bwd.
+ * mea_matmul_gated_act_fwd, mea_matmul_gated_act_bwd; mea_matmul.
  */
 #ifndef MEA_BLOCK_H
 #define MEA_BLOCK_H
@@ -128,6 +128,21 @@ MEA_API mea_status_t mea_matmul_gated_act_fwd(mea_act_t act, int64_t M, int64_t 
 MEA_API mea_status_t mea_matmul_gated_act_bwd(mea_act_t act, int64_t M, int64_t N, int64_t K, const void *g,
                                               const void *w_down, const void *z, float param, void *dz,
                                               void *h, mea_stream_t stream);
+
+/* Matrix product C = op(A) op(B) in bf16 with fp32 accumulation on the tensor
+ * cores, each operand read as it is stored: the products around the gated
+ * block (h Wd^T; dz [Wg; Wu]; dz^T X and G^T h) without a transposed copy.
+ *   trans_a      zero: A is [M x K]; non-zero: A is [K x M] and op(A) = A^T.
+ *   trans_b      zero: B is [K x N]; non-zero: B is [N x K] and op(B) = B^T.
+ *                Both non-zero is MEA_ERR_UNSUPPORTED.
+ *   M, N, K      each below 2^31; M or N of 0 is a no-op, K of 0 sets C to
+ *                zero.  The rows of A, B and C as stored must be multiples of
+ *                8 elements (else MEA_ERR_UNSUPPORTED).
+ *   a, b         device, bf16, row-major, read only, 16-byte aligned.
+ *   c            device, bf16, [M x N], written, 16-byte aligned; overlaps
+ *                neither operand. */
+MEA_API mea_status_t mea_matmul(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K, const void *a,
+                                const void *b, void *c, mea_stream_t stream);
 
 #ifdef __cplusplus
 }

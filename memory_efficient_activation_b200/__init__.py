@@ -12,6 +12,7 @@ Functions (the C ABI's names without the ``mea_`` prefix):
     act_fwd, act_bwd, affine_swish_fwd, affine_swish_bwd,
     affine_act_fwd, affine_act_bwd, swish_channel_fwd, swish_channel_bwd,
     matmul_act_fwd, matmul_act_bwd, matmul_gated_act_fwd, matmul_gated_act_bwd,
+    matmul,
     norm_fwd, norm_bwd,
     concat_bn_relu_fwd, concat_bn_relu_apply, concat_bn_relu_bwd,
     act_fwd_bwd_host,
@@ -41,7 +42,7 @@ __all__ = [
     "act_fwd", "act_bwd", "act_fwd_grouped", "act_bwd_grouped", "affine_swish_fwd", "affine_swish_bwd",
     "affine_act_fwd", "affine_act_bwd", "swish_channel_fwd", "swish_channel_bwd",
     "swish_channel_fwd_grouped", "swish_channel_bwd_grouped", "swish_channel_bwd_grouped_workspace_bytes",
-    "matmul_act_fwd", "matmul_act_bwd", "matmul_gated_act_fwd", "matmul_gated_act_bwd",
+    "matmul_act_fwd", "matmul_act_bwd", "matmul_gated_act_fwd", "matmul_gated_act_bwd", "matmul",
     "GatedMLPFunction", "MemoryEfficientGatedMLP",
     "norm_fwd", "norm_bwd", "norm_bwd_workspace_bytes",
     "NormFunction", "MemoryEfficientLayerNorm", "MemoryEfficientRMSNorm",
@@ -625,6 +626,24 @@ def matmul_gated_act_bwd(act: str, g: torch.Tensor, w_down: torch.Tensor, z: tor
     return dz, h
 
 
+def matmul(a: torch.Tensor, b: torch.Tensor, trans_a: bool = False, trans_b: bool = False,
+           out: torch.Tensor | None = None) -> torch.Tensor:
+    """op(a) op(b) in bf16 on the tensor cores, each operand read as it is
+    stored: a [M, K] ([K, M] with trans_a), b [K, N] ([N, K] with trans_b), not
+    both transposed.  The stored rows must be multiples of 8 elements."""
+    _mat2d(a, "a")
+    _mat2d(b, "b")
+    K, M = a.shape if trans_a else a.shape[::-1]
+    N, Kb = b.shape if trans_b else b.shape[::-1]
+    if Kb != K:
+        raise ValueError("a and b disagree in K")
+    if b.device != a.device:
+        raise ValueError("a and b must be on the same device")
+    c = a.new_empty((M, N)) if out is None else _shaped(out, (M, N), torch.bfloat16, a.device, "out")
+    _call("mea_matmul", a, int(trans_a), int(trans_b), M, N, K, a.data_ptr(), b.data_ptr(), c.data_ptr())
+    return c
+
+
 def _norm_id(norm: str) -> int:
     try:
         return NORM_IDS[norm]
@@ -1137,7 +1156,7 @@ def _gated_mlp(x, w_gate_up, w_down, gamma, beta, act, param, norm, eps, keep: b
     H = w_gate_up.shape[0] // 2
     n, mean, invstd = (x, None, None) if norm is None else norm_fwd(norm, x, gamma, beta, eps, want_stats=keep)
     z, h = matmul_gated_act_fwd(act, n, w_gate_up[:H], w_gate_up[H:], param, want_z=keep)
-    return torch.matmul(h, w_down.t()), mean, invstd, z
+    return matmul(h, w_down, trans_b=True), mean, invstd, z
 
 
 class GatedMLPFunction(torch.autograd.Function):
@@ -1147,8 +1166,8 @@ class GatedMLPFunction(torch.autograd.Function):
     and product are one kernel; the backward multiplies dout Wd by the
     product's derivatives inside the matmul that forms it, in which h is
     re-populated, and forms n again from x.  The other products (h Wd^T;
-    dWd = dout^T h, d[Wg; Wu] = dz^T n, dn = dz [Wg; Wu]) are plain matmuls
-    (torch.matmul).  w_gate_up [2 d_hidden, d_model] holds Wg above Wu."""
+    dWd = dout^T h, d[Wg; Wu] = dz^T n, dn = dz [Wg; Wu]) are plain ones
+    (matmul).  w_gate_up [2 d_hidden, d_model] holds Wg above Wu."""
 
     @staticmethod
     def forward(ctx, x, w_gate_up, w_down, gamma, beta, act: str, param: float, norm: str | None, eps: float):
@@ -1166,16 +1185,16 @@ class GatedMLPFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         dout = dout.contiguous()
         dz, h = matmul_gated_act_bwd(act, dout, w_down, z, param, want_h=need[2])
-        dw_down = torch.matmul(dout.t(), h) if need[2] else None
+        dw_down = matmul(dout, h, trans_a=True) if need[2] else None
         del h
         dw1 = None
         if need[1]:
             n = x if norm is None else norm_fwd(norm, x, gamma, beta, eps, want_stats=False)[0]
-            dw1 = torch.matmul(dz.t(), n)
+            dw1 = matmul(dz, n, trans_a=True)
             del n
         dx = dgamma = dbeta = None
         if need[0] or need[3] or need[4]:
-            dx = torch.matmul(dz, w_gate_up)
+            dx = matmul(dz, w_gate_up)
             if norm is not None:
                 dx, dgamma, dbeta = norm_bwd(norm, x, dx, gamma, mean, invstd, want_dgamma=need[3], want_dbeta=need[4],
                                              out=dx)

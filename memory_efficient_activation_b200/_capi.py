@@ -98,6 +98,7 @@ BLOCK_SIGNATURES = {
     "mea_norm_bwd": (_i, [_i, _i, _i, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mea_matmul_gated_act_fwd": (_i, [_i, _i64, _i64, _i64, _vp, _vp, _vp, _f, _vp, _vp, _vp]),
     "mea_matmul_gated_act_bwd": (_i, [_i, _i64, _i64, _i64, _vp, _vp, _vp, _f, _vp, _vp, _vp]),
+    "mea_matmul": (_i, [_i, _i, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None

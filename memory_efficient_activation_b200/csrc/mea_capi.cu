@@ -800,6 +800,32 @@ mea_status_t mea_matmul_gated_act_bwd(mea_act_t act, int64_t M, int64_t N, int64
     return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul_gated_act_bwd launch");
 }
 
+mea_status_t mea_matmul(int trans_a, int trans_b, int64_t M, int64_t N, int64_t K, const void *a, const void *b,
+                        void *c, mea_stream_t stream)
+{
+    Range range_("mea_matmul");
+    clear_error();
+    mea_status_t st = check_matmul("", MEA_RELU, M, N, K);
+    if (st != MEA_OK) return st;
+    if (trans_a && trans_b) return fail(MEA_ERR_UNSUPPORTED, "both operands transposed is not served");
+    if (M == 0 || N == 0) return MEA_OK;
+    if (!c) return fail(MEA_ERR_INVALID_ARG, "c is NULL");
+    if (N % 8 || (trans_a && M % 8) || ((!trans_a || trans_b) && K % 8))
+        return fail(MEA_ERR_UNSUPPORTED, "the rows of a, b and c must be multiples of 8 elements");
+    if (!aligned16(c)) return fail(MEA_ERR_UNSUPPORTED, "a, b and c must be 16-byte aligned");
+    const size_t ba = (size_t)M * K * 2, bb = (size_t)N * K * 2, bc = (size_t)M * N * 2;
+    if (K == 0) {
+        cudaError_t e = cudaMemsetAsync(c, 0, bc, reinterpret_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul");
+    }
+    if (!a || !b) return fail(MEA_ERR_INVALID_ARG, "a or b is NULL");
+    if (!aligned16(a) || !aligned16(b)) return fail(MEA_ERR_UNSUPPORTED, "a, b and c must be 16-byte aligned");
+    if (overlaps(c, bc, a, ba) || overlaps(c, bc, b, bb)) return fail(MEA_ERR_INVALID_ARG, "c overlaps a or b");
+    mea::MatmulPlain p{trans_a != 0, trans_b != 0, M, N, K, a, b, c, reinterpret_cast<cudaStream_t>(stream)};
+    cudaError_t e = mea::launch_matmul(p);
+    return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul launch");
+}
+
 static mea_status_t check_norm(int norm, int dtype, int pdtype, int64_t rows, int64_t C)
 {
     if (norm != MEA_LAYER_NORM && norm != MEA_RMS_NORM)

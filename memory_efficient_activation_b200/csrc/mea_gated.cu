@@ -31,6 +31,7 @@
 // sets g_gated_error and the roles stop issuing work.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "mea_device.cuh"
@@ -46,31 +47,59 @@ __device__ unsigned int g_gated_error = 0;
 
 namespace {
 
+// What a kernel computes: the two passes of the gated block, or the plain
+// product C = op(A) op(B)^T around it, with A stored [M x K] or [K x M] and B
+// stored [N x K] or [K x N].
+enum Mode { kFwd, kBwd, kPlainNT, kPlainNN, kPlainTN };
+
 constexpr int kBM = 256;                                    // rows of a CTA pair's tile
 constexpr int kAcc = 256;                                   // accumulator columns per CTA
 constexpr int kBK = 64;                                     // K per pipeline stage: 128 bytes
 constexpr int kHalf = 128;                                  // rows (columns) of A and B one CTA stages
 constexpr int kUmmaK = 16;
-constexpr int kStages = 7;
-constexpr int kThreadsG = 192;
 constexpr int kGroupM = 8;                                  // row tiles per group of the tile order
 constexpr uint32_t kStageA = kHalf * kBK * 2;               // 16 KB
 constexpr uint32_t kStageBytes = 2 * kStageA;
 constexpr uint32_t kTmemCols = 2 * kAcc;                    // 512: all of tensor memory
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 256;
 
-// Instruction descriptor (kind::f16): fp32 accumulator, A and B bf16, A
-// K-major, B K-major (forward) or N-major (backward, bit 16), N 256, M 256.
+// Epilogue chunk: a warp's 32 rows x 32 columns of one tensor, 64 bytes per
+// row in shared memory under the 64-byte swizzle, moved by TMA.
+constexpr uint32_t kChunk = 32 * 32 * 2;
+
+template <Mode MODE>
+struct Shape {
+    static constexpr bool kMMajorA = MODE == kPlainTN;
+    static constexpr bool kNMajorB = MODE == kBwd || MODE == kPlainNN || MODE == kPlainTN;
+    static constexpr int kTN = MODE == kFwd ? kHalf : kAcc;              // output columns of a tile
+    // Epilogue warps: one per quarter of tensor memory.  Eight for the backward
+    // (each half of the columns) hide more latency but take 40 KB more of
+    // chunk buffers, one pipeline stage: slower (at [4096 x 10928 x 2048] 220
+    // us against 196).
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    // Chunk buffers per warp.  Backward: gate and up as they arrive (read into
+    // registers at once, so that the next chunk's loads fly during this one's
+    // arithmetic), dgate, dup and h.  Forward: gate, up and h.  Plain: two of
+    // C in turn.
+    static constexpr int kChunks = MODE == kBwd ? 5 : MODE == kFwd ? 3 : 2;
+    static constexpr uint32_t kEpiBytes = kWarps * kChunks * kChunk;
+    // Pipeline stages: what is left of the shared memory.
+    static constexpr int kStages = MODE == kBwd ? 5 : 6;
+    static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiBytes + 256;
+    static_assert(kSmemBytes <= 232448, "shared memory of a block");
+};
+
+// Instruction descriptor (kind::f16): fp32 accumulator, A and B bf16, N 256,
+// M 256; A K-major or M-major (bit 15), B K-major or N-major (bit 16).
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kAcc >> 3) << 17) |
                             ((uint32_t)(kBM >> 4) << 24);
-constexpr uint32_t kIdescNMajor = kIdesc | (1u << 16);
 
-// Shared-memory descriptor of an N-major operand tile written by TMA with the
-// 128-byte swizzle: each k row holds 64 contiguous elements of N (128 bytes),
-// 8-row groups of k lie 1024 bytes apart (stride byte offset), and the next
-// 64 elements of N lie 64 x 128 = 8192 bytes on (leading byte offset).  A K
-// step of 16 advances the start address by 16 rows, 2048 bytes.
-__device__ __forceinline__ uint64_t sdesc_nmajor(uint32_t saddr)
+// Shared-memory descriptor of an M- or N-major operand tile written by TMA
+// with the 128-byte swizzle: each k row holds 64 contiguous elements of M or N
+// (128 bytes), 8-row groups of k lie 1024 bytes apart (stride byte offset),
+// and the next 64 elements lie 64 x 128 = 8192 bytes on (leading byte
+// offset).  A K step of 16 advances the start address by 16 rows, 2048 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr)
 {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
@@ -88,26 +117,56 @@ __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int &tm
     tm = g * kGroupM + r - tn * rows;
 }
 
-// 32 bf16 as 16 words, from or to a 16-byte aligned place, the first ncols (a
-// multiple of 8) of them.
-__device__ __forceinline__ void load32(const uint16_t *p, int ncols, uint32_t (&w)[16])
+// Row `lane` of a chunk in shared memory, 32 bf16 as 16 words.  The 64-byte
+// swizzle exchanges the 16-byte quarters of a row by bits 1-2 of its number,
+// so a warp's accesses touch every bank once per quarter.
+__device__ __forceinline__ uint32_t chunk_quarter(uint32_t chunk, int lane, int q)
 {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint4 v = 8 * q < ncols ? *(reinterpret_cast<const uint4 *>(p) + q) : make_uint4(0, 0, 0, 0);
-        w[4 * q] = v.x;
-        w[4 * q + 1] = v.y;
-        w[4 * q + 2] = v.z;
-        w[4 * q + 3] = v.w;
-    }
+    return chunk + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
 }
-__device__ __forceinline__ void store32(uint16_t *p, int ncols, const uint32_t (&w)[16])
+__device__ __forceinline__ void load_row(uint32_t chunk, int lane, uint32_t (&w)[16])
 {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        if (8 * q < ncols)
-            st_v4(reinterpret_cast<uint4 *>(p) + q, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * q]), "=r"(w[4 * q + 1]), "=r"(w[4 * q + 2]), "=r"(w[4 * q + 3])
+                     : "r"(chunk_quarter(chunk, lane, q))
+                     : "memory");
 }
+__device__ __forceinline__ void store_row(uint32_t chunk, int lane, const uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(chunk_quarter(chunk, lane, q)), "r"(w[4 * q]),
+                     "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                     : "memory");
+}
+
+// TMA copies of a chunk: this CTA's shared memory to and from [row x col].
+__device__ __forceinline__ void chunk_load(uint32_t dst, const CUtensorMap *map, int col, int row, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void chunk_store(const CUtensorMap *map, int col, int row, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(col), "r"(row), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread's stores have read their source.
+template <int N>
+__device__ __forceinline__ void store_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+// This thread's writes to shared memory become visible to TMA.
+__device__ __forceinline__ void fence_to_tma() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -126,90 +185,186 @@ __device__ __forceinline__ void act32(const float (&v)[32], const Coef &k, float
     }
 }
 
-// Forward epilogue of 32 hidden units of one row.
+// Forward: h = f(gate) up of 32 hidden units of one row, in words.
 template <class A>
-__device__ __forceinline__ void epilogue_fwd(const uint32_t (&ga)[32], const uint32_t (&ua)[32], const Coef &k,
-                                             uint16_t *z, uint16_t *h, int64_t N, int ncols)
+__device__ __forceinline__ void product_fwd(const uint32_t (&ga)[32], const uint32_t (&ua)[32], const Coef &k,
+                                            uint32_t (&w)[16])
 {
-    uint32_t w[16];
-    if (z) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(__uint_as_float(ga[2 * j]), __uint_as_float(ga[2 * j + 1]));
-        store32(z, ncols, w);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(__uint_as_float(ua[2 * j]), __uint_as_float(ua[2 * j + 1]));
-        store32(z + N, ncols, w);
-    }
-    if (h) {
-        float g[32], r[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) g[j] = __uint_as_float(ga[j]);
-        act32<A>(g, k, r);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            w[j] = pack_bf16x2(r[2 * j] * __uint_as_float(ua[2 * j]), r[2 * j + 1] * __uint_as_float(ua[2 * j + 1]));
-        store32(h, ncols, w);
-    }
-}
-
-// Backward epilogue of 32 hidden units of one row.  dz may be zin.
-template <class A>
-__device__ __forceinline__ void epilogue_bwd(const uint32_t (&acc)[32], const Coef &k, const uint16_t *zin,
-                                             uint16_t *dz, uint16_t *h, int64_t N, int ncols)
-{
-    uint32_t gw[16], uw[16], w[16];
-    load32(zin, ncols, gw);
-    load32(zin + N, ncols, uw);
     float g[32], r[32];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        g[2 * j] = lo_f(gw[j]);
-        g[2 * j + 1] = hi_f(gw[j]);
-    }
+    for (int j = 0; j < 32; ++j) g[j] = __uint_as_float(ga[j]);
     act32<A>(g, k, r);
-    if (h) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(r[2 * j] * lo_f(uw[j]), r[2 * j + 1] * hi_f(uw[j]));
-        store32(h, ncols, w);
-    }
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-        w[j] = pack_bf16x2(r[2 * j] * __uint_as_float(acc[2 * j]), r[2 * j + 1] * __uint_as_float(acc[2 * j + 1]));
-    store32(dz + N, ncols, w);
-    bool tail = false;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float d = __uint_as_float(acc[j]) * (j & 1 ? hi_f(uw[j >> 1]) : lo_f(uw[j >> 1]));
-        r[j] = A::template df<false>(g[j], d, k, tail);
-    }
-    if (tail) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (A::template is_tail_bwd<false>(g[j], k))
-                r[j] = A::template df_tail<false>(
-                    g[j], __uint_as_float(acc[j]) * (j & 1 ? hi_f(uw[j >> 1]) : lo_f(uw[j >> 1])), k);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(r[2 * j], r[2 * j + 1]);
-    store32(dz, ncols, w);
+        w[j] = pack_bf16x2(r[2 * j] * __uint_as_float(ua[2 * j]), r[2 * j + 1] * __uint_as_float(ua[2 * j + 1]));
 }
 
-template <class A, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
-gated_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w0,
-             const __grid_constant__ CUtensorMap tma_w1, int M, int N, int K, float param, const uint16_t *zin,
-             uint16_t *z, uint16_t *h)
+__device__ __forceinline__ void pack32(const uint32_t (&a)[32], uint32_t (&w)[16])
 {
-    constexpr int kTN = MODE == 0 ? kHalf : kAcc;          // hidden units of a tile
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
+}
+
+// f and f' of two values from one set of exponentials and reciprocals, in
+// packed pairs: the backward needs both of every element.  `tail` is set where
+// either leaves its main path; the elements that is_tail (f) and is_tail_bwd
+// (f') name are then taken again in scalar form.
+template <class A>
+struct Both {
+    static __device__ __forceinline__ void eval(float x0, float x1, const Coef &k, bool &tail, F2 &f, F2 &df)
+    {
+        f = pk(A::template f<false>(x0, k, tail), A::template f<false>(x1, k, tail));
+        df = pk(A::template df<false>(x0, 1.f, k, tail), A::template df<false>(x1, 1.f, k, tail));
+    }
+};
+// s = 1 / (1 + E), E = 2^t: f = x s, f' = s (1 + alpha x E s), E s = Sigmoid(-alpha x).
+template <bool RC>
+struct Both<SwishT<RC>> {
+    static __device__ __forceinline__ void eval(float x0, float x1, const Coef &k, bool &tail, F2 &f, F2 &df)
+    {
+        const F2 x = pk(x0, x1);
+        float t0, t1, a0, a1;
+        upk(mul2(x, sp2(k.c_hi)), t0, t1);
+        const F2 E = pk(ex2_ftz(t0), ex2_ftz(t1));
+        tail |= fmaxf(t0, t1) > kTailT;
+        if constexpr (RC)
+            tail |= fminf(fabsf(__fsub_rn(t0, SwishT<RC>::kRootT)), fabsf(__fsub_rn(t1, SwishT<RC>::kRootT))) <
+                    SwishT<RC>::kRootWinT;
+        upk(add2(E, sp2(1.f)), a0, a1);
+        const F2 s = pk(rcp_ftz(a0), rcp_ftz(a1));
+        f = mul2(x, s);
+        df = mul2(s, fma2(mul2(x, sp2(k.p)), mul2(E, s), sp2(1.f)));
+    }
+};
+// The same with t a cubic and x v' for alpha x (x beyond 2e10 in size, where
+// x v' could overflow, is tail on the positive side by t < -kHugeT).
+template <>
+struct Both<GeluTanh> {
+    static __device__ __forceinline__ void eval(float x0, float x1, const Coef &, bool &tail, F2 &f, F2 &df)
+    {
+        const F2 x = pk(x0, x1), x2 = mul2(x, x);
+        float t0, t1, a0, a1;
+        upk(mul2(x, fma2(sp2(GeluTanh::kC3f), x2, sp2(GeluTanh::kC1f))), t0, t1);
+        const F2 E = pk(ex2_ftz(t0), ex2_ftz(t1));
+        tail |= (fmaxf(t0, t1) > kTailT) | (fminf(t0, t1) < -GeluTanh::kHugeT);
+        upk(add2(E, sp2(1.f)), a0, a1);
+        const F2 s = pk(rcp_ftz(a0), rcp_ftz(a1));
+        f = mul2(x, s);
+        const F2 q = mul2(x, fma2(sp2(GeluTanh::kK3x3f), x2, sp2(GeluTanh::kK1f)));
+        df = mul2(s, fma2(q, mul2(E, s), sp2(1.f)));
+    }
+};
+// Phi(x) by the backward's erfc (one Gaussian for it and for x phi(x)).
+template <>
+struct Both<GeluErf> {
+    static __device__ __forceinline__ void eval(float x0, float x1, const Coef &, bool &tail, F2 &f, F2 &df)
+    {
+        const F2 x = pk(x0, x1), w = mul2(x, sp2(GeluErf::kNegRsqrt2Hi));
+        float w0, w1, d0, d1, v0, v1, a0, a1;
+        upk(w, w0, w1);
+        upk(add2(pk(fabsf(w0), fabsf(w1)), sp2(2.0f)), d0, d1);
+        const F2 h = pk(rcp_ftz(d0), rcp_ftz(d1));
+        upk(mul2(mul2(w, w), sp2(-GeluErf::kLog2ef)), v0, v1);
+        tail |= fminf(x0, x1) < GeluErf::kTailX;
+        const F2 g = pk(ex2_ftz(v0), ex2_ftz(v1));
+        upk(mul2(mul2(h, GeluErf::q8_2(h)), g), a0, a1);
+        const F2 phi = pk(w0 >= 0.f ? a0 : 1.f - a0, w1 >= 0.f ? a1 : 1.f - a1);
+        f = mul2(x, phi);
+        df = fma2(mul2(x, sp2(GeluErf::kRsqrt2Pi)), g, phi);
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_f2(F2 v)
+{
+    float a, b;
+    upk(v, a, b);
+    return pack_bf16x2(a, b);
+}
+
+// One element again, where it may have left the main path: e its place in the
+// pair (0 low, 1 high).
+template <class A>
+__device__ __forceinline__ void bwd_again(uint32_t gw, uint32_t uw, float d, int e, const Coef &k, float &dg, float &du,
+                                          float &h)
+{
+    const float g = e ? hi_f(gw) : lo_f(gw), u = e ? hi_f(uw) : lo_f(uw);
+    if (A::is_tail(g, k)) {
+        const float f = A::template f_tail<false>(g, k);
+        du = f * d;
+        h = f * u;
+    }
+    if (A::template is_tail_bwd<false>(g, k)) dg = A::template df_tail<false>(g, d * u, k);
+}
+
+// Backward of 32 hidden units of one row: gw, uw the stored gate and up, in
+// place of which dgate and dup are returned; hw the product.
+template <class A>
+__device__ __forceinline__ void product_bwd(const uint32_t (&acc)[32], const Coef &k, uint32_t (&gw)[16],
+                                            uint32_t (&uw)[16], uint32_t (&hw)[16])
+{
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        uint32_t dg[8], du[8];
+        bool tail = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = 8 * p + j;
+            const F2 u = pk(lo_f(uw[i]), hi_f(uw[i]));
+            const F2 d = pk(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
+            F2 f, df;
+            Both<A>::eval(lo_f(gw[i]), hi_f(gw[i]), k, tail, f, df);
+            hw[i] = pack_f2(mul2(f, u));
+            du[j] = pack_f2(mul2(f, d));
+            dg[j] = pack_f2(mul2(mul2(d, u), df));
+        }
+        if (tail) {
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = 8 * p + j;
+                    float vg = e ? hi_f(dg[j]) : lo_f(dg[j]), vu = e ? hi_f(du[j]) : lo_f(du[j]),
+                          vh = e ? hi_f(hw[i]) : lo_f(hw[i]);
+                    bwd_again<A>(gw[i], uw[i], __uint_as_float(e ? acc[2 * i + 1] : acc[2 * i]), e, k, vg, vu, vh);
+                    dg[j] = e ? pack_bf16x2(lo_f(dg[j]), vg) : pack_bf16x2(vg, hi_f(dg[j]));
+                    du[j] = e ? pack_bf16x2(lo_f(du[j]), vu) : pack_bf16x2(vu, hi_f(du[j]));
+                    hw[i] = e ? pack_bf16x2(lo_f(hw[i]), vh) : pack_bf16x2(vh, hi_f(hw[i]));
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            gw[8 * p + j] = dg[j];
+            uw[8 * p + j] = du[j];
+        }
+    }
+}
+
+// Tensor maps of a launch.  Forward: x, w0 = Wg, w1 = Wu, out0 and out1 the
+// halves of z, out2 = h.  Backward: x = G, w0 = Wd, in0 and in1 the halves of
+// the stored z, out0 and out1 those of dz, out2 = h.  Plain: x = A, w0 = B,
+// out0 = C.
+struct Maps {
+    CUtensorMap x, w0, w1, in0, in1, out0, out1, out2;
+};
+
+template <class A, Mode MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThreads, 1)
+gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param, int want01, int want2)
+{
+    using S = Shape<MODE>;
+    constexpr int kTN = S::kTN, kStages = S::kStages;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);   // 1024-byte aligned tiles
     const uint32_t sbase = smem_addr(smem);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);
+    const uint32_t ebase = sbase + kStages * kStageBytes;  // epilogue chunks
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + S::kEpiBytes);
     uint64_t *empty = full + kStages;
     uint64_t *acc_full = empty + kStages;
     uint64_t *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *in_full = acc_empty + 2;                     // backward: a chunk of z has landed, per warp
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(in_full + S::kWarps);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();          // 0: issues the MMAs of the pair
@@ -225,8 +380,9 @@ gated_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(acc_full + b), 1);
-            mbar_init(smem_addr(acc_empty + b), 8); // four epilogue warps of each CTA
+            mbar_init(smem_addr(acc_empty + b), 2 * S::kWarps);   // the epilogue warps of both CTAs
         }
+        for (int i = 0; i < S::kWarps; ++i) mbar_init(smem_addr(in_full + i), 1);
         mbar_init_fence();
     }
     if (warp == 1) {
@@ -258,14 +414,24 @@ gated_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ 
                     const uint32_t fb = cluster_addr(smem_addr(full + s), 0);
                     if (rank == 0) mbar_arrive_expect_tx(smem_addr(full + s), 2 * kStageBytes);
                     const uint32_t sa = sbase + s * kStageBytes, sb = sa + kStageA;
-                    tma_load_2d_pair(sa, &tma_x, kb * kBK, tm * kBM + rank * kHalf, fb);
-                    if constexpr (MODE == 0) {
-                        tma_load_2d_pair(sb, rank == 0 ? &tma_w0 : &tma_w1, kb * kBK, tn * kTN, fb);
+                    const int ra = tm * kBM + rank * kHalf;
+                    if constexpr (S::kMMajorA) {
+                        // two boxes of 64 k rows x 64 elements of M
+                        tma_load_2d_pair(sa, &maps.x, ra, kb * kBK, fb);
+                        tma_load_2d_pair(sa + kStageA / 2, &maps.x, ra + 64, kb * kBK, fb);
                     } else {
-                        // two boxes of 64 k rows x 64 columns of Wd
+                        tma_load_2d_pair(sa, &maps.x, kb * kBK, ra, fb);
+                    }
+                    if constexpr (MODE == kFwd) {
+                        tma_load_2d_pair(sb, rank == 0 ? &maps.w0 : &maps.w1, kb * kBK, tn * kTN, fb);
+                    } else {
                         const int c = tn * kTN + rank * kHalf;
-                        tma_load_2d_pair(sb, &tma_w0, c, kb * kBK, fb);
-                        tma_load_2d_pair(sb + kStageA / 2, &tma_w0, c + 64, kb * kBK, fb);
+                        if constexpr (S::kNMajorB) {
+                            tma_load_2d_pair(sb, &maps.w0, c, kb * kBK, fb);
+                            tma_load_2d_pair(sb + kStageA / 2, &maps.w0, c + 64, kb * kBK, fb);
+                        } else {
+                            tma_load_2d_pair(sb, &maps.w0, kb * kBK, c, fb);
+                        }
                     }
                 }
             }
@@ -297,11 +463,10 @@ gated_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ 
                     const uint32_t sa = sbase + s * kStageBytes, sb = sa + kStageA;
 #pragma unroll
                     for (int k = 0; k < kBK / kUmmaK; ++k) {
-                        const uint64_t da = sdesc_sw128(sa + k * kUmmaK * 2);
-                        if constexpr (MODE == 0)
-                            umma_bf16_pair(d, da, sdesc_sw128(sb + k * kUmmaK * 2), kIdesc, (kb | k) != 0);
-                        else
-                            umma_bf16_pair(d, da, sdesc_nmajor(sb + k * kUmmaK * 128), kIdescNMajor, (kb | k) != 0);
+                        constexpr uint32_t idesc = kIdesc | (S::kMMajorA ? 1u << 15 : 0u) | (S::kNMajorB ? 1u << 16 : 0u);
+                        const uint64_t da = S::kMMajorA ? sdesc_mn(sa + k * kUmmaK * 128) : sdesc_sw128(sa + k * kUmmaK * 2);
+                        const uint64_t db = S::kNMajorB ? sdesc_mn(sb + k * kUmmaK * 128) : sdesc_sw128(sb + k * kUmmaK * 2);
+                        umma_bf16_pair(d, da, db, idesc, (kb | k) != 0);
                     }
                     umma_commit_pair(smem_addr(empty + s));
                 }
@@ -311,41 +476,132 @@ gated_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ 
         __syncwarp();
     } else {
         // epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31 of
-        // this CTA, i.e. rows rank * 128 + 32 (w % 4) + lane of the tile
-        const int q = warp & 3;
+        // this CTA, i.e. rows rank * 128 + 32 (w % 4) + lane of the tile, in
+        // chunks of 32 columns.  Results (and the backward's z) pass through
+        // the warp's own chunk buffers, moved by TMA: a thread owns a row, and
+        // 16-byte accesses of 32 rows straight to global memory took 32
+        // cache lines an instruction, more time than the matmul at K 2048.
+        const int q = warp & 3, ew = warp - 2;
         const Coef k = A::coef(param);
         const uint32_t release = cluster_addr(smem_addr(acc_empty), 0);
+        const uint32_t mine = ebase + ew * (S::kChunks * kChunk);
+        constexpr int kHalves = S::kWarps / 4, kMost = kTN / 32 / kHalves;   // column shares, chunks of one
+        const int c0 = (ew >> 2) * kMost;                  // this warp's first chunk
+        const uint32_t in_bar = smem_addr(in_full + ew);
+        const int row_in = (int)rank * kHalf + q * 32;
+        // chunks of tile t with something in them, from c0 on
+        auto chunks = [&](int t) {
+            int tm, tn;
+            tile_of(t, tiles_m, tiles_n, tm, tn);
+            if (tm * kBM + row_in >= M) return 0;
+            const int left = (N - tn * kTN + 31) / 32 - c0;
+            return left < 0 ? 0 : left < kMost ? left : kMost;
+        };
+        auto fetch = [&](int t, int c) {                   // backward: z of a chunk
+            if (lane == 0) {
+                int tm, tn;
+                tile_of(t, tiles_m, tiles_n, tm, tn);
+                const int col = tn * kTN + (c0 + c) * 32, row = tm * kBM + row_in;
+                mbar_arrive_expect_tx(in_bar, 2 * kChunk);
+                chunk_load(mine, &maps.in0, col, row, in_bar);
+                chunk_load(mine + kChunk, &maps.in1, col, row, in_bar);
+            }
+        };
+        int n = 0;                                         // chunks taken so far
+        bool ok = true, ahead = false;                     // ahead: chunk n is on its way
+        if constexpr (MODE == kBwd) {
+            for (int t = pair; t < ntiles && !ahead; t += npairs)
+                if (chunks(t) > 0) {
+                    fetch(t, 0);
+                    ahead = true;
+                }
+        }
         int lt = 0;
         for (int t = pair; t < ntiles; t += npairs, ++lt) {
             const int b = lt & 1, use = lt >> 1;
             if (!mbar_wait(smem_addr(acc_full + b), use & 1)) {
                 record_error();
-                break;
+                ok = false;
             }
+            if (!ok) break;
             tc_fence_after();
             int tm, tn;
             tile_of(t, tiles_m, tiles_n, tm, tn);
-            const int row = tm * kBM + (int)rank * kHalf + q * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + b * kAcc;
+            const int row = tm * kBM + row_in, nc = chunks(t);
 #pragma unroll 1
-            for (int c = 0; c < kTN / 32; ++c) {
-                uint32_t v[32], u[32];
-                tmem_ld32(lanes + c * 32, v);
-                if constexpr (MODE == 0) tmem_ld32(lanes + kHalf + c * 32, u);
-                const int col = tn * kTN + c * 32;
-                if (row < M && col < N) {
-                    const int ncols = N - col < 32 ? N - col : 32;
-                    const int64_t oz = (int64_t)row * 2 * N + col, oh = (int64_t)row * N + col;
-                    if constexpr (MODE == 0)
-                        epilogue_fwd<A>(v, u, k, z ? z + oz : nullptr, h ? h + oh : nullptr, N, ncols);
-                    else
-                        epilogue_bwd<A>(v, k, zin + oz, z + oz, h ? h + oh : nullptr, N, ncols);
+            for (int c = 0; c < nc; ++c, ++n) {
+                uint32_t v[32], w[16];
+                tmem_ld32(lanes + (c0 + c) * 32, v);
+                const int col = tn * kTN + (c0 + c) * 32;
+                const uint32_t buf = mine + (MODE == kBwd ? 2 : MODE == kFwd ? 0 : n & 1) * kChunk;
+                if constexpr (MODE == kFwd) {
+                    uint32_t u[32];
+                    tmem_ld32(lanes + kHalf + (c0 + c) * 32, u);
+                    if (lane == 0) store_wait_read<0>();
+                    __syncwarp();
+                    if (want01) {
+                        pack32(v, w);
+                        store_row(buf, lane, w);
+                        pack32(u, w);
+                        store_row(buf + kChunk, lane, w);
+                    }
+                    if (want2) {
+                        product_fwd<A>(v, u, k, w);
+                        store_row(buf + 2 * kChunk, lane, w);
+                    }
+                } else if constexpr (MODE == kBwd) {
+                    uint32_t uw[16], hw[16];
+                    ahead = false;
+                    if (!mbar_wait(in_bar, n & 1)) {
+                        record_error();
+                        ok = false;
+                        break;
+                    }
+                    load_row(mine, lane, w);
+                    load_row(mine + kChunk, lane, uw);
+                    __syncwarp();
+                    int nt = t, nx = c + 1;                // the next chunk's z
+                    if (nx == nc) {
+                        nx = 0;
+                        do nt += npairs;
+                        while (nt < ntiles && chunks(nt) == 0);
+                    }
+                    if (nt < ntiles) {
+                        fetch(nt, nx);
+                        ahead = true;
+                    }
+                    product_bwd<A>(v, k, w, uw, hw);
+                    if (lane == 0) store_wait_read<0>();   // of the chunk before: long done
+                    __syncwarp();
+                    store_row(buf, lane, w);
+                    store_row(buf + kChunk, lane, uw);
+                    if (want2) store_row(buf + 2 * kChunk, lane, hw);
+                } else {
+                    pack32(v, w);
+                    if (lane == 0) store_wait_read<1>();
+                    __syncwarp();
+                    store_row(buf, lane, w);
+                }
+                fence_to_tma();
+                __syncwarp();
+                if (lane == 0) {
+                    if (MODE != kFwd || want01) chunk_store(&maps.out0, col, row, buf);
+                    if constexpr (MODE == kFwd || MODE == kBwd) {
+                        if (want01) chunk_store(&maps.out1, col, row, buf + kChunk);
+                        if (want2) chunk_store(&maps.out2, col, row, buf + 2 * kChunk);
+                    }
+                    store_commit();
                 }
             }
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(release + 8 * b);
         }
+        // what is in flight has landed before this CTA's memory goes away
+        if (ahead && !mbar_wait(in_bar, n & 1)) record_error();
+        if (lane == 0) store_wait_read<0>();
     }
     pdl_trigger();
     tc_fence_before();
@@ -358,31 +614,46 @@ gated_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ 
 
 // ------------------------------------------------------------ host side
 
-template <class A, int MODE>
+// 2-D map of one [rows x cols] bf16 tensor with row stride ld (elements) for
+// the epilogue's chunks: box of 32 x 32, 64-byte swizzle.
+bool chunk_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld)
+{
+    return bf16_map(map, base, rows, cols, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <class A, Mode MODE>
 cudaError_t launch_one(const GatedLaunch &a)
 {
-    CUtensorMap mx, mw0, mw1;
-    bool ok = bf16_tile_map(&mx, a.x, a.M, a.K, kHalf);
-    if (MODE == 0) {
-        ok = ok && bf16_tile_map(&mw0, a.w0, a.N, a.K, kHalf) && bf16_tile_map(&mw1, a.w1, a.N, a.K, kHalf);
+    using S = Shape<MODE>;
+    Maps m;
+    // an operand stored with K contiguous: boxes of 128 rows x 64 k; one with
+    // M or N contiguous: boxes of 64 k x 64
+    bool ok = S::kMMajorA ? bf16_tile_map(&m.x, a.x, a.K, a.M, kBK) : bf16_tile_map(&m.x, a.x, a.M, a.K, kHalf);
+    ok = ok && (S::kNMajorB ? bf16_tile_map(&m.w0, a.w0, a.K, a.N, kBK) : bf16_tile_map(&m.w0, a.w0, a.N, a.K, kHalf));
+    m.w1 = m.in0 = m.in1 = m.out0 = m.out1 = m.out2 = m.w0;
+    const uint16_t *zin = static_cast<const uint16_t *>(a.zin);
+    uint16_t *z = static_cast<uint16_t *>(a.z);
+    if (MODE == kFwd) ok = ok && bf16_tile_map(&m.w1, a.w1, a.N, a.K, kHalf);
+    if (MODE == kBwd)
+        ok = ok && chunk_map(&m.in0, zin, a.M, a.N, 2 * a.N) && chunk_map(&m.in1, zin + a.N, a.M, a.N, 2 * a.N);
+    if (MODE == kFwd || MODE == kBwd) {
+        if (z) ok = ok && chunk_map(&m.out0, z, a.M, a.N, 2 * a.N) && chunk_map(&m.out1, z + a.N, a.M, a.N, 2 * a.N);
+        if (a.h) ok = ok && chunk_map(&m.out2, a.h, a.M, a.N, a.N);
     } else {
-        ok = ok && bf16_tile_map(&mw0, a.w0, a.K, a.N, kBK);
-        mw1 = mw0;
+        ok = ok && chunk_map(&m.out0, z, a.M, a.N, a.N);
     }
     if (!ok) return cudaErrorInvalidValue;
     auto kernel = gated_kernel<A, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int tn = MODE == 0 ? kHalf : kAcc;
-    const int64_t tiles = ((a.M + kBM - 1) / kBM) * ((a.N + tn - 1) / tn);
+    const int64_t tiles = ((a.M + kBM - 1) / kBM) * ((a.N + S::kTN - 1) / S::kTN);
     const int pairs_max = sm_count() / 2;
     const int pairs = (int)(tiles < pairs_max ? tiles : pairs_max);
-    return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(kThreadsG), kSmemBytes, a.stream, mx, mw0, mw1,
-                      (int)a.M, (int)a.N, (int)a.K, a.param, static_cast<const uint16_t *>(a.zin),
-                      static_cast<uint16_t *>(a.z), static_cast<uint16_t *>(a.h));
+    return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(S::kThreads), S::kSmemBytes, a.stream, m, (int)a.M,
+                      (int)a.N, (int)a.K, a.param, (int)(z != nullptr), (int)(a.h != nullptr));
 }
 
-template <int MODE>
+template <Mode MODE>
 cudaError_t by_act(const GatedLaunch &a)
 {
     switch (a.act) {
@@ -392,7 +663,13 @@ cudaError_t by_act(const GatedLaunch &a)
     case 3: return launch_one<Tanh, MODE>(a);
     case 4: return launch_one<GeluErf, MODE>(a);
     case 5: return launch_one<GeluTanh, MODE>(a);
-    case 6: return launch_one<Swish, MODE>(a);
+    case 6: {
+        // f alone has no zero of f' to guard, nor has f' where alpha is a power
+        // of two: bf16 inputs then keep their distance from it
+        int e;
+        const bool pow2 = a.param == 0.f || fabsf(frexpf(a.param, &e)) == 0.5f;
+        return MODE == kFwd || pow2 ? launch_one<SwishT<false>, MODE>(a) : launch_one<SwishT<true>, MODE>(a);
+    }
     }
     return cudaErrorInvalidValue;
 }
@@ -409,6 +686,20 @@ cudaError_t gated_error_word(int clear, unsigned int *word)
     return e;
 }
 
-cudaError_t launch_gated(const GatedLaunch &a) { return a.mode == 0 ? by_act<0>(a) : by_act<1>(a); }
+cudaError_t launch_gated(const GatedLaunch &a) { return a.mode == 0 ? by_act<kFwd>(a) : by_act<kBwd>(a); }
+
+cudaError_t launch_matmul(const MatmulPlain &p)
+{
+    GatedLaunch a{};
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.x = p.a;
+    a.w0 = p.b;
+    a.z = p.c;
+    a.stream = p.stream;
+    if (p.trans_a) return launch_one<ReLU, kPlainTN>(a);
+    return p.trans_b ? launch_one<ReLU, kPlainNT>(a) : launch_one<ReLU, kPlainNN>(a);
+}
 
 }  // namespace mea

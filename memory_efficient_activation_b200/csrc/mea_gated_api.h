@@ -29,6 +29,19 @@ struct GatedLaunch {
     cudaStream_t stream;
 };
 
+// Plain product C [M x N] = op(A) op(B), bf16, fp32 accumulation: A is [M x K]
+// (or [K x M] with trans_a), B is [K x N] (or [N x K] with trans_b); not both
+// transposed.
+struct MatmulPlain {
+    int trans_a, trans_b;
+    int64_t M, N, K;
+    const void *a;
+    const void *b;
+    void *c;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_matmul(const MatmulPlain &p);
 cudaError_t launch_gated(const GatedLaunch &a);
 cudaError_t gated_error_word(int clear, unsigned int *word);   // synchronous
 

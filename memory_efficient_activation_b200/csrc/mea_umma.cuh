@@ -119,9 +119,11 @@ inline EncodeTiled tensor_map_encoder()
     return fn;
 }
 
-// 2-D map of a row-major bf16 [rows x cols] matrix, box of box_rows x 64,
-// 128-byte swizzle, zeros beyond the edges.
-inline bool bf16_tile_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, uint32_t box_rows)
+// 2-D map of a row-major bf16 [rows x cols] matrix with a row stride of ld
+// elements, box of box_rows x box_cols, zeros read beyond the edges and
+// nothing written there.
+inline bool bf16_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows,
+                     uint32_t box_cols, CUtensorMapSwizzle swizzle)
 {
     EncodeTiled enc = tensor_map_encoder();
     // The encoder is a driver call and needs the device's context current on
@@ -130,12 +132,18 @@ inline bool bf16_tile_map(CUtensorMap *map, const void *base, int64_t rows, int6
     int dev = 0;
     if (!enc || cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The operand tile of a matmul: box of box_rows x 64, 128-byte swizzle.
+inline bool bf16_tile_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, uint32_t box_rows)
+{
+    return bf16_map(map, base, rows, cols, cols, box_rows, 64, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace mea

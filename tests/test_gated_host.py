@@ -115,3 +115,30 @@ def test_binding_refuses_cpu_tensors():
         mea.matmul_gated_act_fwd("swish", x, x, x)
     with pytest.raises(ValueError):
         mea.matmul_gated_act_bwd("swish", x, torch.zeros(8, 8, dtype=torch.bfloat16), torch.zeros(5, 16, dtype=torch.bfloat16))
+
+
+def test_matmul_validation(lib):
+    def mm(ta=0, tb=0, M=8, N=16, K=24, a=P, b=2 * P, c=3 * P):
+        return lib.mea_matmul(ta, tb, M, N, K, a, b, c, None)
+
+    assert mm(ta=1, tb=1) == UNS and mm(M=-1) == INV and mm(N=1 << 31) == UNS
+    assert mm(a=None) == INV and mm(b=None) == INV and mm(c=None) == INV
+    assert mm(a=P + 8) == UNS and mm(b=2 * P + 8) == UNS and mm(c=3 * P + 8) == UNS
+    assert mm(N=12) == UNS and mm(K=12) == UNS and mm(ta=1, M=12) == UNS and mm(tb=1, K=12) == UNS
+    assert mm(c=P) == INV and mm(c=2 * P + 16) == INV
+    assert mm(M=0) == OK and mm(N=0) == OK
+
+
+def test_matmul_binding_checks(monkeypatch):
+    fake = _FakeLib()
+    monkeypatch.setattr(_capi, "lib", lambda: fake)
+    monkeypatch.setattr(mea, "_need_cuda", lambda *ts: None)
+    monkeypatch.setattr(mea, "_stream", lambda t: 0)
+    bf = torch.bfloat16
+    a, b = torch.zeros(5, 8, dtype=bf), torch.zeros(8, 16, dtype=bf)
+    assert mea.matmul(a, b).shape == (5, 16) and mea.matmul(b, b, True).shape == (16, 16)
+    assert mea.matmul(a, torch.zeros(24, 8, dtype=bf), trans_b=True).shape == (5, 24)
+    for call in (lambda: mea.matmul(a, a), lambda: mea.matmul(a, b, True), lambda: mea.matmul(a[0], b),
+                 lambda: mea.matmul(a, b, out=torch.empty(5, 8, dtype=bf))):
+        with pytest.raises(ValueError):
+            call()

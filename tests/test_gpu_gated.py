@@ -280,3 +280,36 @@ def test_gated_block_training_step_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("M,N,K", [(8, 8, 8), (256, 256, 64), (264, 520, 72), (2056, 1032, 136), (4104, 2728, 264),
+                                   (1, 40, 16), (37, 264, 200), (1000, 328, 1)])
+def test_matmul_layouts(ta, tb, M, N, K):
+    """Plain product in the three layouts, odd M (K with the first operand
+    transposed): K additions in fp32 and one rounding."""
+    if ta:
+        M, K = -(-M // 8) * 8, K - 7 if K > 8 else K
+    elif K % 8:
+        K = 8
+    g = _gen(M + N + K)
+    a = _normal(g, *((K, M) if ta else (M, K)))
+    b = _normal(g, *((N, K) if tb else (K, N)))
+    c = mea.matmul(a, b, ta, tb)
+    A, B = a.t() if ta else a, b.t() if tb else b
+    want = A.double() @ B.double()
+    e = K * 2.0 ** -23 * (A.double().abs() @ B.double().abs())
+    ref.assert_within(c, want, e + 2.0 ** -8 * (want.abs() + e) + ref.TINY, "c")
+    ref.assert_close_overall(c, want, "c")
+    assert torch.equal(c, mea.matmul(a, b, ta, tb))
+
+
+def test_matmul_empty_and_guarded():
+    a, b = torch.empty(0, 16, dtype=BF, device="cuda"), torch.ones(16, 24, dtype=BF, device="cuda")
+    assert mea.matmul(a, b).shape == (0, 24)
+    z = mea.matmul(torch.empty(0, 16, dtype=BF, device="cuda"), torch.empty(0, 24, dtype=BF, device="cuda"), True)
+    assert z.shape == (16, 24) and not z.any()
+    buf = torch.full((37 * 40 + 128,), 7.0, dtype=BF, device="cuda")
+    mea.matmul(torch.ones(37, 16, dtype=BF, device="cuda"), torch.ones(16, 40, dtype=BF, device="cuda"),
+               out=buf[64:64 + 37 * 40].view(37, 40))
+    assert (buf[:64] == 7).all() and (buf[-64:] == 7).all() and (buf[64:-64] == 16).all()
