@@ -20,23 +20,30 @@
 
 #include "mea_device.cuh"
 #include "mea_internal.h"
+#include "mea_math.cuh"
 #include "mea_norm_api.h"
+#include "mea_pipe.cuh"
 #include "mea_stream.cuh"
 
 namespace mea {
+
+__device__ unsigned int g_norm_error = 0;   // a bounded barrier wait expired
+
 namespace {
 
 constexpr int kNormThreads = 256;      // threads of a block (more where one row needs more)
 constexpr int kNormMaxThreads = 1024;
 constexpr int kSlabRows = 1024;        // most rows whose terms one fp32 column sum takes
 constexpr int kSlabs = 296;            // column-sum slabs of a large tensor (two per SM)
+constexpr int64_t kRingBytes = 4 << 20;   // the forward streams through a ring from this size of x on
 constexpr int kColX = 32, kColY = 8;   // threads of a column-sum block: columns x rows
 
-// Column-sum slabs: a function of the row count only, so the order of the
-// sums does not depend on the device.
-inline int64_t norm_slabs(int64_t rows)
+// Column-sum slabs, from the row count and the rows a block takes at a time
+// only, so the order of the sums does not depend on the device: two blocks
+// per SM, at least two rounds of rows each, at most kSlabRows rows.
+inline int64_t norm_slabs(int64_t rows, int at_a_time)
 {
-    int64_t s = (rows + kColY - 1) / kColY;
+    int64_t s = (rows + 2 * at_a_time - 1) / (2 * at_a_time);
     if (s > kSlabs) s = kSlabs;
     const int64_t m = (rows + kSlabRows - 1) / kSlabRows;
     if (s < m) s = m;
@@ -85,13 +92,22 @@ __device__ __forceinline__ void load_params(const void *p, int64_t i, float fill
     }
 }
 
+// Sum over the 2^lg (at most 32) neighbouring threads of a warp that share a
+// row, in each of them.
+__device__ __forceinline__ float lanes_sum(float v, int lg)
+{
+#pragma unroll
+    for (int b = 0; b < 5; ++b)
+        if (b < lg) v += __shfl_xor_sync(0xffffffffu, v, 1 << b);
+    return v;
+}
+
 // Sum over the group of 2^lg threads that owns a row, in every thread of the
 // group.  Groups of more than a warp exchange through red (one float per
 // warp), between two barriers that every thread of the block takes.
 __device__ __forceinline__ float group_sum(float v, int lg, float *red)
 {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    v = lanes_sum(v, lg);
     if (lg > 5) {
         const int warp = threadIdx.x >> 5, wpg = 1 << (lg - 5), first = warp & ~(wpg - 1);
         __syncthreads();
@@ -103,10 +119,144 @@ __device__ __forceinline__ float group_sum(float v, int lg, float *red)
     return v;
 }
 
+// Arithmetic on the elements of an item, two at a time in packed .f32x2
+// instructions (the one-pass kernels are near the issue limit without them).
+template <int VL>
+__device__ __forceinline__ void v_center(float (&x)[VL], float m, float s)   // (x - m) s
+{
+    if constexpr (VL == 1) {
+        x[0] = (x[0] - m) * s;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2) upk(mul2(add2(pk(x[e], x[e + 1]), sp2(-m)), sp2(s)), x[e], x[e + 1]);
+    }
+}
+template <int VL>
+__device__ __forceinline__ void v_mul(const float (&a)[VL], const float (&b)[VL], float (&o)[VL])
+{
+    if constexpr (VL == 1) {
+        o[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2) upk(mul2(pk(a[e], a[e + 1]), pk(b[e], b[e + 1])), o[e], o[e + 1]);
+    }
+}
+template <int VL>
+__device__ __forceinline__ void v_fma(const float (&a)[VL], const float (&b)[VL], float (&o)[VL])   // o += a b
+{
+    if constexpr (VL == 1) {
+        o[0] = fmaf(a[0], b[0], o[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2)
+            upk(fma2(pk(a[e], a[e + 1]), pk(b[e], b[e + 1]), pk(o[e], o[e + 1])), o[e], o[e + 1]);
+    }
+}
+template <int VL>
+__device__ __forceinline__ void v_add(const float (&a)[VL], float (&o)[VL])   // o += a
+{
+    if constexpr (VL == 1) {
+        o[0] += a[0];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2) upk(add2(pk(a[e], a[e + 1]), pk(o[e], o[e + 1])), o[e], o[e + 1]);
+    }
+}
+// Two partial sums of the elements, and of the products.
+template <int VL>
+__device__ __forceinline__ void v_sum(const float (&a)[VL], float (&s)[2])
+{
+    if constexpr (VL == 1) {
+        s[0] += a[0];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2) upk(add2(pk(a[e], a[e + 1]), pk(s[0], s[1])), s[0], s[1]);
+    }
+}
+template <int VL>
+__device__ __forceinline__ void v_dot(const float (&a)[VL], const float (&b)[VL], float (&s)[2])
+{
+    if constexpr (VL == 1) {
+        s[0] = fmaf(a[0], b[0], s[0]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2)
+            upk(fma2(pk(a[e], a[e + 1]), pk(b[e], b[e + 1]), pk(s[0], s[1])), s[0], s[1]);
+    }
+}
+// is ((p - h m2) - m1), over p
+template <int VL>
+__device__ __forceinline__ void v_dx(float (&p)[VL], const float (&h)[VL], float m1, float m2, float is)
+{
+    if constexpr (VL == 1) {
+        p[0] = is * (fmaf(-h[0], m2, p[0]) - m1);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2)
+            upk(mul2(add2(fma2(pk(h[e], h[e + 1]), sp2(-m2), pk(p[e], p[e + 1])), sp2(-m1)), sp2(is)), p[e], p[e + 1]);
+    }
+}
+
+// ------------------------------------------------------------- row rings
+//
+// The one-pass kernels: a block takes a run of consecutive rows, S at a time
+// (G threads to a row, T = S G threads), through a ring of stages in shared
+// memory that 1-D bulk copies fill (rows are contiguous: one copy per tensor
+// and stage), far enough ahead that a row reduction's barrier does not show.
+// A thread keeps the same columns of every row it sees, NV items of VL
+// elements, so gamma and beta (and the backward's column sums) stay in
+// registers.  Copies start and end on 16-byte boundaries: a stage whose rows
+// do not is copied from the boundary before it (its elements then lie `skew`
+// further on) to the one after, except at the very end of the tensor, whose
+// last few elements are read directly.
+//
+// G is a power of two up to a warp, or a number of whole warps.
+struct RingGeo {
+    int G, S, nv;            // threads to a row, rows at a time, items per thread
+};
+
+// Item access in a stage.
+template <typename T, int VL>
+struct RingItem {
+    static constexpr int64_t q = 16 / Store<T>::kBytes;
+    // First element and bytes of the copy for elements [a, b) of a tensor of
+    // `end` elements.
+    static __device__ __forceinline__ void span(int64_t a, int64_t b, int64_t end, int64_t &first, uint32_t &n)
+    {
+        first = a / q * q;
+        const int64_t up = (b + q - 1) / q * q;
+        n = (uint32_t)(((up <= end ? up : b / q * q) - first) * Store<T>::kBytes);
+    }
+    // Item i of the row that starts at element `base` of the tensor p, skew
+    // elements into the stage of n bytes.
+    static __device__ __forceinline__ void load(const unsigned char *stage, uint32_t n, int skew, const void *p,
+                                                int64_t base, int i, float (&f)[VL])
+    {
+        if constexpr (VL == 1)
+            f[0] = (uint32_t)(skew + i + 1) * Store<T>::kBytes <= n ? load1_rw<T>(stage, skew + i)
+                                                                    : load1_rw<T>(p, base + i);
+        else
+            Store<T>::unpack(reinterpret_cast<const uint4 *>(stage)[skew / VL + i], f);
+    }
+};
+
+// Sum over the warps of a row: `own` (one float per warp of the block) holds
+// each warp's sum, the row's begin at w0.
+__device__ __forceinline__ float warps_sum(const float *own, int w0, int wpg)
+{
+    const int lane = threadIdx.x & 31;
+    float v = lane < wpg ? own[w0 + lane] : 0.f;
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
+__device__ __forceinline__ int lane_bits(int G) { return G >= 32 ? 5 : __ffs(G) - 1; }
+
 // ---------------------------------------------------------------- forward
 
-template <typename T, typename TP, bool RMS, int VL, int NV>
-__global__ void __launch_bounds__(kNormMaxThreads)
+template <typename T, typename TP, bool RMS, int VL, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 norm_fwd_kernel(const void *__restrict__ x, const void *__restrict__ gamma, const void *__restrict__ beta, float eps,
                 void *__restrict__ y, float *__restrict__ mean_out, float *__restrict__ invstd_out, int64_t rows,
                 int64_t C, int lg)
@@ -167,6 +317,179 @@ norm_fwd_kernel(const void *__restrict__ x, const void *__restrict__ gamma, cons
             for (int e = 0; e < VL; ++e) f[e] = fmaf((f[e] - mean) * invstd, w[e], b[e]);
             It::store(y, base + g + j * G, f);
         }
+}
+
+template <int VL, int NV>
+struct FwdRing {
+    static constexpr int kThreads = 256;           // at most
+    static constexpr bool kKeep = VL * NV <= 16;   // gamma and beta in registers
+    static constexpr int kBlocks = kKeep ? 3 : 2;  // per SM
+    template <typename T>
+    static constexpr uint32_t bytes = (uint32_t)kThreads * NV * VL * Store<T>::kBytes + 32;
+    template <typename T>
+    static constexpr int stages = (int)((kKeep ? 72u : 108u) * 1024 / bytes<T>) < 8
+                                      ? (int)((kKeep ? 72u : 108u) * 1024 / bytes<T>)
+                                      : 8;
+    template <typename T>
+    static constexpr size_t smem = (size_t)stages<T> * bytes<T>;
+};
+
+// Forward of a run of rows.  Layer norm's variance needs the mean first; to
+// take one barrier instead of two, every warp forms the sum of its own
+// elements and their squared distances from the warp's own mean, and the
+// row's warps are merged exactly (Chan, Golub and LeVeque, "Updating formulae
+// and a pairwise algorithm for computing sample variances", 1979):
+//   M2 = sum M2_w + sum n_w (mean_w - mean)^2.
+template <typename T, typename TP, bool RMS, int VL, int NV>
+__global__ void __launch_bounds__(256, FwdRing<VL, NV>::kBlocks)
+norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma, const void *__restrict__ beta,
+                     float eps, void *__restrict__ y, float *__restrict__ mean_out, float *__restrict__ invstd_out,
+                     int64_t rows, int64_t C, int G, int S, int64_t per_block)
+{
+    using F = FwdRing<VL, NV>;
+    using R = RingItem<T, VL>;
+    constexpr int kRing = F::template stages<T>, eb = Store<T>::kBytes;
+    constexpr uint32_t kBytes = F::template bytes<T>;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[kRing];
+    __shared__ float red[2][2][8];
+    const int tid = threadIdx.x, slot = tid / G, g = tid - slot * G, lb = lane_bits(G), wpg = G >> 5;
+    const int w0 = slot * wpg, lane = tid & 31;
+    const int items = (int)(C / VL);
+    const int64_t r0 = (int64_t)blockIdx.x * per_block, r1 = r0 + per_block < rows ? r0 + per_block : rows;
+    const int steps = r1 > r0 ? (int)((r1 - r0 + S - 1) / S) : 0;
+    const float rc = 1.f / (float)C;
+    if (tid == 0) {
+        for (int s = 0; s < kRing; ++s) mbar_init(smem_addr(full + s), 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    pdl_wait();
+    auto span = [&](int s, int64_t &first, uint32_t &n) {
+        const int64_t a = r0 + (int64_t)s * S, b = a + S < r1 ? a + S : r1;
+        R::span(a * C, b * C, rows * C, first, n);
+    };
+    auto fill = [&](int s) {
+        int64_t first;
+        uint32_t n;
+        span(s, first, n);
+        const uint32_t bar = smem_addr(full + s % kRing);
+        mbar_arrive_expect_tx(bar, n);
+        if (n) bulk_load(smem_addr(ring) + s % kRing * kBytes, static_cast<const unsigned char *>(x) + first * eb, n, bar);
+    };
+    if (tid == 0)
+        for (int s = 0; s < kRing && s < steps; ++s) fill(s);
+
+    float wk[F::kKeep ? NV : 1][VL], bk[F::kKeep ? NV : 1][VL];
+    int mine = 0;                                  // this thread's elements of a row
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (g + j * G < items) {
+            mine += VL;
+            if constexpr (F::kKeep) {
+                load_params<TP, VL>(gamma, g + j * G, 1.f, wk[j]);
+                load_params<TP, VL>(beta, g + j * G, 0.f, bk[j]);
+            }
+        }
+    // elements of this warp's part of the row (of the whole row for a group
+    // within a warp), and of the warp that this lane merges
+    const float nw = lanes_sum((float)mine, lb), rnw = nw > 0.f ? 1.f / nw : 0.f;
+    float nl = 0.f;
+    if (!RMS && G > 32) {
+        if (lane == 0) red[0][0][tid >> 5] = nw;
+        __syncthreads();
+        nl = lane < wpg ? red[0][0][w0 + lane] : 0.f;
+        __syncthreads();
+    }
+    int64_t row = r0 + slot;
+    for (int s = 0; s < steps; ++s, row += S) {
+        const int st = s % kRing;
+        if (!mbar_wait(smem_addr(full + st), (s / kRing) & 1)) atomicExch(&g_norm_error, 1u);
+        const bool live = row < r1;
+        float h[NV][VL];
+        float t[2] = {0.f, 0.f};
+        int64_t first;
+        uint32_t n;
+        span(s, first, n);
+        if (live) {
+            const int skew = (int)(row * C - first);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (g + j * G < items) {
+                    R::load(ring + st * kBytes, n, skew, x, row * C, g + j * G, h[j]);
+                    if (RMS)
+                        v_dot(h[j], h[j], t);
+                    else
+                        v_sum(h[j], t);
+                }
+        }
+        float mean = 0.f, m2;
+        if constexpr (RMS) {
+            m2 = lanes_sum(t[0] + t[1], lb);
+        } else {
+            mean = lanes_sum(t[0] + t[1], lb) * rnw;
+            t[0] = t[1] = 0.f;
+            if (live) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (g + j * G < items) {
+                        float c[VL];
+#pragma unroll
+                        for (int e = 0; e < VL; ++e) c[e] = h[j][e];
+                        v_center(c, mean, 1.f);
+                        v_dot(c, c, t);
+                    }
+            }
+            m2 = lanes_sum(t[0] + t[1], lb);
+        }
+        if (G > 32 && lane == 0) {
+            red[s & 1][0][tid >> 5] = mean;
+            red[s & 1][1][tid >> 5] = m2;
+        }
+        __syncthreads();                           // the rows' sums, and every thread has left the stage
+        if (tid == 0 && s + kRing < steps) fill(s + kRing);
+        if (G > 32) {
+            if constexpr (RMS) {
+                m2 = warps_sum(red[s & 1][1], w0, wpg);
+            } else {
+                const float mw = lane < wpg ? red[s & 1][0][w0 + lane] : 0.f;
+                const float qw = lane < wpg ? red[s & 1][1][w0 + lane] : 0.f;
+                float v = mw * nl;
+#pragma unroll
+                for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                mean = __shfl_sync(0xffffffffu, v, 0) * rc;
+                v = fmaf((mw - mean) * (mw - mean), nl, qw);
+#pragma unroll
+                for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                m2 = __shfl_sync(0xffffffffu, v, 0);
+            }
+        }
+        if (!live) continue;
+        const float is = rsqrtf(fmaf(m2, rc, eps));
+        if (g == 0) {
+            if (!RMS && mean_out) mean_out[row] = mean;
+            if (invstd_out) invstd_out[row] = is;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (g + j * G < items) {
+                float w[VL], b[VL];
+                if constexpr (F::kKeep) {
+#pragma unroll
+                    for (int e = 0; e < VL; ++e) {
+                        w[e] = wk[j][e];
+                        b[e] = bk[j][e];
+                    }
+                } else {
+                    load_params<TP, VL>(gamma, g + j * G, 1.f, w);
+                    load_params<TP, VL>(beta, g + j * G, 0.f, b);
+                }
+                v_center(h[j], mean, is);
+                v_fma(h[j], w, b);
+                Item<T, VL>::store(y, row * items + g + j * G, b);
+            }
+    }
+    pdl_trigger();
 }
 
 // Rows too long for the registers of a block: one block per row, which is
@@ -287,6 +610,175 @@ norm_finish_kernel(const float *__restrict__ partial, void *__restrict__ dgamma,
     }
 }
 
+// dx and the column sums of one slab of rows in one pass over x and dy.
+template <int VL, int NV>
+struct BwdRing {
+    static constexpr int kThreads = 512;           // at most
+    static constexpr bool kKeep = VL * NV <= 8;    // gamma in registers (64 of them: two blocks per SM)
+    static constexpr int kBlocks = kKeep ? 2 : 1;
+    template <typename T>
+    static constexpr uint32_t bytes = (uint32_t)kThreads * NV * VL * Store<T>::kBytes + 32;   // of one tensor
+    template <typename T>
+    static constexpr int stages = (int)((kKeep ? 100u : 200u) * 1024 / (2 * bytes<T>)) < 8
+                                      ? (int)((kKeep ? 100u : 200u) * 1024 / (2 * bytes<T>))
+                                      : 8;
+    template <typename T>
+    static constexpr size_t smem = (size_t)stages<T> * 2 * bytes<T>;
+};
+
+template <typename T, typename TP, bool RMS, int VL, int NV>
+__global__ void __launch_bounds__(512, BwdRing<VL, NV>::kBlocks)
+norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gamma, const float *__restrict__ mean_in,
+                     const float *__restrict__ invstd_in, void *dx, float *__restrict__ partial, int64_t rows,
+                     int64_t C, int G, int S, int64_t per_slab)
+{
+    using F = BwdRing<VL, NV>;
+    using R = RingItem<T, VL>;
+    constexpr int kRing = F::template stages<T>, eb = Store<T>::kBytes;
+    constexpr uint32_t kBytes = F::template bytes<T>;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[kRing];
+    __shared__ float red[2][2][16];
+    const int tid = threadIdx.x, slot = tid / G, g = tid - slot * G, lb = lane_bits(G), wpg = G >> 5, w0 = slot * wpg;
+    const int items = (int)(C / VL);
+    const int64_t r0 = (int64_t)blockIdx.x * per_slab, r1 = r0 + per_slab < rows ? r0 + per_slab : rows;
+    const int steps = r1 > r0 ? (int)((r1 - r0 + S - 1) / S) : 0;
+    const float rc = 1.f / (float)C;
+    if (tid == 0) {
+        for (int s = 0; s < kRing; ++s) mbar_init(smem_addr(full + s), 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    pdl_wait();
+    auto span = [&](int s, int64_t &first, uint32_t &n) {
+        const int64_t a = r0 + (int64_t)s * S, b = a + S < r1 ? a + S : r1;
+        R::span(a * C, b * C, rows * C, first, n);
+    };
+    auto fill = [&](int s) {
+        int64_t first;
+        uint32_t n;
+        span(s, first, n);
+        const uint32_t bar = smem_addr(full + s % kRing), dst = smem_addr(ring) + s % kRing * 2 * kBytes;
+        mbar_arrive_expect_tx(bar, 2 * n);
+        if (n) {
+            bulk_load(dst, static_cast<const unsigned char *>(x) + first * eb, n, bar);
+            bulk_load(dst + kBytes, static_cast<const unsigned char *>(dy) + first * eb, n, bar);
+        }
+    };
+    if (tid == 0)
+        for (int s = 0; s < kRing && s < steps; ++s) fill(s);
+
+    float wk[F::kKeep ? NV : 1][VL], ag[NV][VL], ab[NV][VL];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int e = 0; e < VL; ++e) ag[j][e] = ab[j][e] = 0.f;
+        if constexpr (F::kKeep)
+            if (g + j * G < items) load_params<TP, VL>(gamma, g + j * G, 1.f, wk[j]);
+    }
+    auto weigh = [&](int j, const float (&d)[VL], float (&p)[VL]) {   // p = d gamma
+        if constexpr (F::kKeep) {
+            v_mul(d, wk[j], p);
+        } else {
+            float w[VL];
+            load_params<TP, VL>(gamma, g + j * G, 1.f, w);
+            v_mul(d, w, p);
+        }
+    };
+    int64_t row = r0 + slot;
+    float mean = 0.f, is = 0.f;
+    if (row < r1) {
+        if (!RMS) mean = mean_in[row];
+        is = invstd_in[row];
+    }
+    for (int s = 0; s < steps; ++s, row += S) {
+        const int st = s % kRing;
+        if (!mbar_wait(smem_addr(full + st), (s / kRing) & 1)) atomicExch(&g_norm_error, 1u);
+        const bool live = row < r1;
+        float mean_n = 0.f, is_n = 0.f;            // statistics of the next round
+        if (row + S < r1) {
+            if (!RMS) mean_n = mean_in[row + S];
+            is_n = invstd_in[row + S];
+        }
+        float h[NV][VL], d[NV][VL];                // xhat, dy
+        float t1[2] = {0.f, 0.f}, t2[2] = {0.f, 0.f};
+        if (live) {
+            int64_t first;
+            uint32_t n;
+            span(s, first, n);
+            const int64_t base = row * C;
+            const int skew = (int)(base - first);
+            const unsigned char *sx = ring + st * 2 * kBytes;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (g + j * G < items) {
+                    R::load(sx, n, skew, x, base, g + j * G, h[j]);
+                    R::load(sx + kBytes, n, skew, dy, base, g + j * G, d[j]);
+                    float p[VL];
+                    v_center(h[j], mean, is);
+                    weigh(j, d[j], p);
+                    if (!RMS) v_sum(p, t1);
+                    v_dot(p, h[j], t2);
+                }
+        }
+        float s1 = RMS ? 0.f : lanes_sum(t1[0] + t1[1], lb), s2 = lanes_sum(t2[0] + t2[1], lb);
+        // one barrier a round: the rows' sums are exchanged (in turn between
+        // two buffers), and every thread has left the stage
+        if (G > 32 && (tid & 31) == 0) {
+            red[s & 1][0][tid >> 5] = s1;
+            red[s & 1][1][tid >> 5] = s2;
+        }
+        __syncthreads();
+        if (tid == 0 && s + kRing < steps) fill(s + kRing);
+        if (G > 32) {
+            if (!RMS) s1 = warps_sum(red[s & 1][0], w0, wpg);
+            s2 = warps_sum(red[s & 1][1], w0, wpg);
+        }
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (g + j * G < items) {
+                    float p[VL];
+                    v_fma(d[j], h[j], ag[j]);
+                    v_add(d[j], ab[j]);
+                    weigh(j, d[j], p);
+                    v_dx(p, h[j], s1 * rc, s2 * rc, is);
+                    Item<T, VL>::store(dx, row * items + g + j * G, p);
+                }
+        }
+        mean = mean_n;
+        is = is_n;
+    }
+    pdl_trigger();
+    if (!partial) return;
+    // the S slots' sums of each column, in order
+    float *col = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float *out = partial + ((int64_t)blockIdx.x * 2 + half) * C;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (g + j * G < items)
+#pragma unroll
+                for (int e = 0; e < VL; ++e) {
+                    const int c = (g + j * G) * VL + e;
+                    const float v = half ? ab[j][e] : ag[j][e];
+                    if (S > 1)
+                        col[slot * (int)C + c] = v;
+                    else
+                        out[c] = v;
+                }
+        if (S == 1) continue;
+        __syncthreads();
+        for (int c = tid; c < (int)C; c += blockDim.x) {
+            float t = 0.f;
+            for (int k = 0; k < S; ++k) t += col[k * (int)C + c];
+            out[c] = t;
+        }
+    }
+}
+
 // dx of one row per group of threads.  dx may be x or dy itself: every
 // element is read before it is written, by the thread that writes it.
 template <typename T, typename TP, bool RMS, int VL, int NV>
@@ -398,6 +890,23 @@ inline Group pick_group(int64_t items, int64_t rows, int nv_max)
     return Group{lg, nv <= nv_max ? nv : 0};
 }
 
+// A ring kernel's geometry: `want` items per thread where `most_threads` hold
+// the row so, more (up to `most`) where they do not; false where no number
+// does.
+inline bool ring_geo(int64_t items, int want, int most, int most_threads, RingGeo *r)
+{
+    int nv = 1;
+    while (nv < want && nv < items) nv <<= 1;
+    while (nv <= most && (items + nv - 1) / nv > most_threads) nv <<= 1;
+    if (nv > most) return false;
+    const int need = (int)((items + nv - 1) / nv);
+    int G = 1;
+    while (G < 32 && G < need) G <<= 1;
+    if (need > 32) G = (need + 31) / 32 * 32;
+    *r = RingGeo{G, most_threads / G, nv};
+    return true;
+}
+
 template <typename F>
 cudaError_t by_nv(int nv, F f)
 {
@@ -411,9 +920,45 @@ cudaError_t by_nv(int nv, F f)
     return cudaErrorInvalidValue;
 }
 
+template <typename T, typename TP, bool RMS, int VL, int NV>
+cudaError_t fwd_ring_nv(const NormLaunch &a, const RingGeo &r)
+{
+    using F = FwdRing<VL, NV>;
+    auto kernel = norm_fwd_ring_kernel<T, TP, RMS, VL, NV>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::template smem<T>);
+    if (e != cudaSuccess) return e;
+    int64_t blocks = (a.rows + r.S - 1) / r.S;
+    if (blocks > 148 * F::kBlocks) blocks = 148 * F::kBlocks;
+    const int64_t per = (a.rows + blocks - 1) / blocks;
+    return launch_pdl(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(r.G * r.S), F::template smem<T>, a.stream,
+                      a.x, a.gamma, a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C, r.G, r.S, per);
+}
+
+// The forward's ring: 16 elements of a row per thread, up to 64 (16 one by
+// one).  Few rows take the kernel above it: nothing to stream, and a row
+// spread over more threads answers sooner.
+template <typename T, typename TP, bool RMS, int VL>
+bool fwd_ring(const NormLaunch &a, cudaError_t *e)
+{
+    constexpr int kWant = 16 / VL, kMost = VL == 1 ? 16 : VL == 4 ? 16 : 8;
+    RingGeo r;
+    if (a.rows * a.C * Store<T>::kBytes < kRingBytes || !aligned16(a.x) || !ring_geo(a.C / VL, kWant, kMost, 256, &r))
+        return false;
+    *e = by_nv(r.nv, [&](auto n) -> cudaError_t {
+        constexpr int NV = decltype(n)::value;
+        if constexpr (NV > kMost)
+            return cudaErrorInvalidValue;
+        else
+            return fwd_ring_nv<T, TP, RMS, VL, NV>(a, r);
+    });
+    return true;
+}
+
 template <typename T, typename TP, bool RMS, int VL>
 cudaError_t fwd_vl(const NormLaunch &a)
 {
+    cudaError_t re;
+    if (fwd_ring<T, TP, RMS, VL>(a, &re)) return re;
     const Group g = pick_group(a.C / VL, a.rows, 16);
     if (g.nv == 0)
         return launch_pdl(norm_fwd_long_kernel<T, TP, RMS>, dim3((unsigned)a.rows), dim3(kNormMaxThreads), 0, a.stream,
@@ -421,18 +966,57 @@ cudaError_t fwd_vl(const NormLaunch &a)
     const int threads = (1 << g.lg) > kNormThreads ? (1 << g.lg) : kNormThreads;
     const int64_t per = threads >> g.lg;
     return by_nv(g.nv, [&](auto nv) {
-        return launch_pdl(norm_fwd_kernel<T, TP, RMS, VL, decltype(nv)::value>,
-                          dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads), 0, a.stream, a.x, a.gamma, a.beta,
-                          a.eps, a.out, a.mean, a.invstd, a.rows, a.C, g.lg);
+        constexpr int NV = decltype(nv)::value;
+        auto kernel = threads > kNormThreads ? norm_fwd_kernel<T, TP, RMS, VL, NV, kNormMaxThreads>
+                                             : norm_fwd_kernel<T, TP, RMS, VL, NV, kNormThreads>;
+        return launch_pdl(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads), 0, a.stream, a.x, a.gamma,
+                          a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C, g.lg);
     });
+}
+
+template <typename T, typename TP, bool RMS, int VL, int NV>
+cudaError_t bwd_ring_nv(const NormLaunch &a, const RingGeo &r)
+{
+    using F = BwdRing<VL, NV>;
+    auto kernel = norm_bwd_ring_kernel<T, TP, RMS, VL, NV>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::template smem<T>);
+    if (e != cudaSuccess) return e;
+    const bool sums = a.dgamma || a.dbeta;
+    const int64_t slabs = norm_slabs(a.rows, r.S), per = (a.rows + slabs - 1) / slabs;
+    e = launch_pdl(kernel, dim3((unsigned)slabs), dim3(r.G * r.S), F::template smem<T>, a.stream, a.x, a.dy, a.gamma,
+                   a.mean_in, a.invstd_in, a.out, static_cast<float *>(sums ? a.workspace : nullptr), a.rows, a.C, r.G,
+                   r.S, per);
+    if (e != cudaSuccess || !sums) return e;
+    return launch_pdl(norm_finish_kernel<TP>, dim3((unsigned)((2 * a.C + kColX - 1) / kColX)), dim3(kColX * kColY), 0,
+                      a.stream, static_cast<const float *>(a.workspace), a.dgamma, a.dbeta, a.C, slabs);
+}
+
+// The backward's ring: 8 elements of a row per thread, up to 32 (16 one by
+// one) for rows of more than 512 threads' worth.
+template <typename T, typename TP, bool RMS, int VL>
+bool bwd_ring(const NormLaunch &a, cudaError_t *e)
+{
+    constexpr int kWant = VL >= 8 ? 1 : 8 / VL, kMost = VL == 1 ? 16 : 32 / VL;
+    RingGeo r;
+    if (!aligned16(a.x) || !aligned16(a.dy) || !ring_geo(a.C / VL, kWant, kMost, 512, &r)) return false;
+    *e = by_nv(r.nv, [&](auto n) -> cudaError_t {
+        constexpr int NV = decltype(n)::value;
+        if constexpr (NV > kMost)
+            return cudaErrorInvalidValue;
+        else
+            return bwd_ring_nv<T, TP, RMS, VL, NV>(a, r);
+    });
+    return true;
 }
 
 template <typename T, typename TP, bool RMS, int VL>
 cudaError_t bwd_vl(const NormLaunch &a)
 {
+    cudaError_t fe;
+    if (bwd_ring<T, TP, RMS, VL>(a, &fe)) return fe;
     if (a.dgamma || a.dbeta) {
         float *partial = static_cast<float *>(a.workspace);
-        const int64_t slabs = norm_slabs(a.rows), per = (a.rows + slabs - 1) / slabs;
+        const int64_t slabs = norm_slabs(a.rows, kColY), per = (a.rows + slabs - 1) / slabs;
         const int64_t cb = (a.C + kColX * VL - 1) / (kColX * VL);
         cudaError_t e = launch_pdl(norm_cols_kernel<T, RMS, VL>, dim3((unsigned)(cb * slabs)),
                                    dim3(kColX * kColY), 0, a.stream, a.x, a.dy, a.mean_in, a.invstd_in, partial,
@@ -489,7 +1073,17 @@ cudaError_t by_type(const NormLaunch &a)
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t C)
 {
     if (rows <= 0 || C <= 0) return 0;
-    return (size_t)norm_slabs(rows) * 2 * (size_t)C * sizeof(float);
+    return (size_t)norm_slabs(rows, 1) * 2 * (size_t)C * sizeof(float);
+}
+
+cudaError_t norm_error_word(int clear, unsigned int *word)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_norm_error, sizeof(unsigned int));
+    if (e == cudaSuccess && clear) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_norm_error, &zero, sizeof(unsigned int));
+    }
+    return e;
 }
 
 cudaError_t launch_norm_fwd(const NormLaunch &a) { return by_type<false>(a); }

@@ -32,6 +32,7 @@ struct NormLaunch {
 };
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t C);
+cudaError_t norm_error_word(int clear, unsigned int *word);   // synchronous
 cudaError_t launch_norm_fwd(const NormLaunch &a);
 cudaError_t launch_norm_bwd(const NormLaunch &a);
 
