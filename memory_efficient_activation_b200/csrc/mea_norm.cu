@@ -34,16 +34,16 @@ namespace {
 constexpr int kNormThreads = 256;      // threads of a block (more where one row needs more)
 constexpr int kNormMaxThreads = 1024;
 constexpr int kSlabRows = 1024;        // most rows whose terms one fp32 column sum takes
-constexpr int kSlabs = 296;            // column-sum slabs of a large tensor (two per SM)
+constexpr int kSlabs = 148;            // column-sum slabs of a large tensor (one per SM of a B200)
 constexpr int64_t kRingBytes = 4 << 20;   // the forward streams through a ring from this size of x on
 constexpr int kColX = 32, kColY = 8;   // threads of a column-sum block: columns x rows
 
 // Column-sum slabs, from the row count and the rows a block takes at a time
-// only, so the order of the sums does not depend on the device: two blocks
-// per SM, at least two rounds of rows each, at most kSlabRows rows.
+// only, so the order of the sums does not depend on the device: one block per
+// SM, at least one round of rows each, at most kSlabRows rows.
 inline int64_t norm_slabs(int64_t rows, int at_a_time)
 {
-    int64_t s = (rows + 2 * at_a_time - 1) / (2 * at_a_time);
+    int64_t s = (rows + at_a_time - 1) / at_a_time;
     if (s > kSlabs) s = kSlabs;
     const int64_t m = (rows + kSlabRows - 1) / kSlabRows;
     if (s < m) s = m;
@@ -96,9 +96,12 @@ __device__ __forceinline__ void load_params(const void *p, int64_t i, float fill
 // row, in each of them.
 __device__ __forceinline__ float lanes_sum(float v, int lg)
 {
+    if (lg >= 5) {
 #pragma unroll
-    for (int b = 0; b < 5; ++b)
-        if (b < lg) v += __shfl_xor_sync(0xffffffffu, v, 1 << b);
+        for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    } else {
+        for (int b = 0; b < lg; ++b) v += __shfl_xor_sync(0xffffffffu, v, 1 << b);
+    }
     return v;
 }
 
@@ -129,6 +132,16 @@ __device__ __forceinline__ void v_center(float (&x)[VL], float m, float s)   // 
     } else {
 #pragma unroll
         for (int e = 0; e < VL; e += 2) upk(mul2(add2(pk(x[e], x[e + 1]), sp2(-m)), sp2(s)), x[e], x[e + 1]);
+    }
+}
+template <int VL>
+__device__ __forceinline__ void v_shift(float (&x)[VL], float m)   // x - m
+{
+    if constexpr (VL == 1) {
+        x[0] -= m;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VL; e += 2) upk(add2(pk(x[e], x[e + 1]), sp2(-m)), x[e], x[e + 1]);
     }
 }
 template <int VL>
@@ -184,72 +197,87 @@ __device__ __forceinline__ void v_dot(const float (&a)[VL], const float (&b)[VL]
             upk(fma2(pk(a[e], a[e + 1]), pk(b[e], b[e + 1]), pk(s[0], s[1])), s[0], s[1]);
     }
 }
-// is ((p - h m2) - m1), over p
+// p a + (h b + c), over p
 template <int VL>
-__device__ __forceinline__ void v_dx(float (&p)[VL], const float (&h)[VL], float m1, float m2, float is)
+__device__ __forceinline__ void v_dx(float (&p)[VL], const float (&h)[VL], float a, float b, float c)
 {
     if constexpr (VL == 1) {
-        p[0] = is * (fmaf(-h[0], m2, p[0]) - m1);
+        p[0] = fmaf(p[0], a, fmaf(h[0], b, c));
     } else {
 #pragma unroll
         for (int e = 0; e < VL; e += 2)
-            upk(mul2(add2(fma2(pk(h[e], h[e + 1]), sp2(-m2), pk(p[e], p[e + 1])), sp2(-m1)), sp2(is)), p[e], p[e + 1]);
+            upk(fma2(pk(p[e], p[e + 1]), sp2(a), fma2(pk(h[e], h[e + 1]), sp2(b), sp2(c))), p[e], p[e + 1]);
     }
 }
 
 // ------------------------------------------------------------- row rings
 //
-// The one-pass kernels: a block takes a run of consecutive rows, S at a time
-// (G threads to a row, T = S G threads), through a ring of stages in shared
-// memory that 1-D bulk copies fill (rows are contiguous: one copy per tensor
-// and stage), far enough ahead that a row reduction's barrier does not show.
-// A thread keeps the same columns of every row it sees, NV items of VL
-// elements, so gamma and beta (and the backward's column sums) stay in
-// registers.  Copies start and end on 16-byte boundaries: a stage whose rows
-// do not is copied from the boundary before it (its elements then lie `skew`
-// further on) to the one after, except at the very end of the tensor, whose
-// last few elements are read directly.
+// The one-pass kernels: a block takes a run of consecutive rows through a ring
+// of stages in shared memory that 1-D bulk copies fill (rows are contiguous:
+// one copy per tensor and stage), far enough ahead that a row reduction's
+// barrier does not show.  G threads own a row, NV items of VL elements each,
+// and S = threads / G rows lie side by side.  A thread keeps the same columns
+// of every row it sees, so gamma and beta (and the backward's column sums)
+// stay in registers.
+//
+// Copies start and end on 16-byte boundaries: a stage whose rows do not is
+// copied from the boundary before it (its elements then lie `skew` further
+// on) to the one after, except at the very end of the tensor, whose last few
+// elements are read directly.
 //
 // G is a power of two up to a warp, or a number of whole warps.
 struct RingGeo {
     int G, S, nv;            // threads to a row, rows at a time, items per thread
 };
 
-// Item access in a stage.
+// A thread's view of the stages: where its items lie, step by step.
 template <typename T, int VL>
-struct RingItem {
-    static constexpr int64_t q = 16 / Store<T>::kBytes;
+struct RingView {
+    static constexpr int q = 16 / Store<T>::kBytes;
     // First element and bytes of the copy for elements [a, b) of a tensor of
     // `end` elements.
     static __device__ __forceinline__ void span(int64_t a, int64_t b, int64_t end, int64_t &first, uint32_t &n)
     {
-        first = a / q * q;
-        const int64_t up = (b + q - 1) / q * q;
-        n = (uint32_t)(((up <= end ? up : b / q * q) - first) * Store<T>::kBytes);
+        first = a & ~(int64_t)(q - 1);
+        const int64_t up = (b + q - 1) & ~(int64_t)(q - 1);
+        n = (uint32_t)(((up <= end ? up : b & ~(int64_t)(q - 1)) - first) * Store<T>::kBytes);
     }
-    // Item i of the row that starts at element `base` of the tensor p, skew
-    // elements into the stage of n bytes.
-    static __device__ __forceinline__ void load(const unsigned char *stage, uint32_t n, int skew, const void *p,
-                                                int64_t base, int i, float (&f)[VL])
+    uint32_t at;             // this thread's item 0: elements from the rows' start in the stage
+    uint32_t skew, turn;     // VL 1: elements before the rows' start, and their change per step
+    uint32_t last, n_last;   // VL 1: the step whose copy ends short of its rows, and its bytes
+    __device__ __forceinline__ RingView(int64_t r0, int64_t r1, int64_t rows, int64_t C, int per, int slot, int g, int steps)
     {
-        if constexpr (VL == 1)
-            f[0] = (uint32_t)(skew + i + 1) * Store<T>::kBytes <= n ? load1_rw<T>(stage, skew + i)
-                                                                    : load1_rw<T>(p, base + i);
-        else
-            Store<T>::unpack(reinterpret_cast<const uint4 *>(stage)[skew / VL + i], f);
+        at = (uint32_t)(slot * C) + g * VL;
+        skew = turn = n_last = 0;
+        last = 0xffffffffu;
+        if constexpr (VL == 1) {
+            skew = (uint32_t)((r0 * C) & (q - 1));
+            turn = (uint32_t)((per * C) & (q - 1));
+            if (r1 == rows && steps > 0) {
+                int64_t first;
+                last = steps - 1;
+                span((r0 + (int64_t)last * per) * C, r1 * C, rows * C, first, n_last);
+            }
+        }
+    }
+    __device__ __forceinline__ void next()
+    {
+        if constexpr (VL == 1) skew = (skew + turn) & (q - 1);
+    }
+    // The i-th item after item 0 in the row that starts `off` elements after
+    // this thread's first, from the stage; p is the tensor at item 0 of that
+    // row.
+    __device__ __forceinline__ void load(const unsigned char *stage, int s, const void *p, int i, int off,
+                                         float (&f)[VL]) const
+    {
+        if constexpr (VL == 1) {
+            const uint32_t o = skew + at + off + i;
+            f[0] = s != (int)last || (o + 1) * Store<T>::kBytes <= n_last ? load1_rw<T>(stage, o) : load1_rw<T>(p, i);
+        } else {
+            Store<T>::unpack(*reinterpret_cast<const uint4 *>(stage + (at + off + i * VL) * Store<T>::kBytes), f);
+        }
     }
 };
-
-// Sum over the warps of a row: `own` (one float per warp of the block) holds
-// each warp's sum, the row's begin at w0.
-__device__ __forceinline__ float warps_sum(const float *own, int w0, int wpg)
-{
-    const int lane = threadIdx.x & 31;
-    float v = lane < wpg ? own[w0 + lane] : 0.f;
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return __shfl_sync(0xffffffffu, v, 0);
-}
 
 __device__ __forceinline__ int lane_bits(int G) { return G >= 32 ? 5 : __ffs(G) - 1; }
 
@@ -319,37 +347,88 @@ norm_fwd_kernel(const void *__restrict__ x, const void *__restrict__ gamma, cons
         }
 }
 
-template <int VL, int NV>
+constexpr int kRingThreads = 512;
+
+// Sums over the row's G threads of N values (sums of R rows), N a power of
+// two: returns them in v, in every thread of the group.  Groups within a warp
+// shuffle each value.  Larger ones halve the values at every step of the
+// butterfly until each lane holds part of one, exchange through red (N floats
+// per warp) and the block's barrier, and spread the totals by shuffles.
+// Every thread of the block takes part, once per barrier in turn.
+template <int N>
+__device__ __forceinline__ void reduce_rows(float (&v)[N], int G, int w0, float (*red)[N][16])
+{
+    const int lane = threadIdx.x & 31;
+    if (G < 32) {
+        const int lb = lane_bits(G);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = lanes_sum(v[i], lb);
+        __syncthreads();
+        return;
+    }
+    constexpr int L = N == 8 ? 3 : N == 4 ? 2 : N == 2 ? 1 : 0;
+    static_assert(N == 1 << L, "a power of two of values");
+#pragma unroll
+    for (int b = 0; b < 5; ++b) {
+        const int off = 16 >> b;
+        if (b < L) {
+            const bool hi = lane & off;
+#pragma unroll
+            for (int i = 0; i < (N >> (b + 1)); ++i) {
+                const float keep = hi ? v[i + (N >> (b + 1))] : v[i], give = hi ? v[i] : v[i + (N >> (b + 1))];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+        }
+    }
+    // lane: value lane >> (5 - L)
+    constexpr int kPart = 32 >> L;                 // lanes of one value
+    const int mine = lane / kPart, part = lane % kPart, wpg = G >> 5;
+    if (part == 0) (*red)[mine][threadIdx.x >> 5] = v[0];
+    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; k += kPart < 16 ? kPart : 16)
+        if (part + k < wpg) t += (*red)[mine][w0 + part + k];
+#pragma unroll
+    for (int off = kPart / 2; off >= 1; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * kPart);
+}
+
+// Forward of a run of rows, 16 elements of a row per thread where they fit.
+// Layer norm's variance needs the mean first; to take one barrier instead of
+// two, every warp forms the sum of its own elements and their squared
+// distances from the warp's own mean, and the row's warps are merged exactly
+// (Chan, Golub and LeVeque, "Updating formulae and a pairwise algorithm for
+// computing sample variances", 1979):
+//   M2 = sum M2_w + sum n_w (mean_w - mean)^2.
+// Blocks of 256 threads, three to an SM (two for long rows): one row at a time
+// and more warps measured better here than the backward's several rows
+// between barriers (16384 x 4096 bf16: 62 against 79 us).
+constexpr int kFwdThreads = 256;
+template <typename T, int VL, int NV>
 struct FwdRing {
-    static constexpr int kThreads = 256;           // at most
     static constexpr bool kKeep = VL * NV <= 16;   // gamma and beta in registers
     static constexpr int kBlocks = kKeep ? 3 : 2;  // per SM
-    template <typename T>
-    static constexpr uint32_t bytes = (uint32_t)kThreads * NV * VL * Store<T>::kBytes + 32;
-    template <typename T>
-    static constexpr int stages = (int)((kKeep ? 72u : 108u) * 1024 / bytes<T>) < 8
-                                      ? (int)((kKeep ? 72u : 108u) * 1024 / bytes<T>)
-                                      : 8;
-    template <typename T>
-    static constexpr size_t smem = (size_t)stages<T> * bytes<T>;
+    static constexpr uint32_t bytes = (uint32_t)kFwdThreads * NV * VL * Store<T>::kBytes + 32;
+    static constexpr int kFit = (int)((kKeep ? 72u : 108u) * 1024 / bytes);
+    static constexpr int stages = kFit < 8 ? kFit : 8;
+    static constexpr size_t smem = (size_t)stages * bytes;
+    static_assert(stages >= 1, "a row");
 };
 
-// Forward of a run of rows.  Layer norm's variance needs the mean first; to
-// take one barrier instead of two, every warp forms the sum of its own
-// elements and their squared distances from the warp's own mean, and the
-// row's warps are merged exactly (Chan, Golub and LeVeque, "Updating formulae
-// and a pairwise algorithm for computing sample variances", 1979):
-//   M2 = sum M2_w + sum n_w (mean_w - mean)^2.
 template <typename T, typename TP, bool RMS, int VL, int NV>
-__global__ void __launch_bounds__(256, FwdRing<VL, NV>::kBlocks)
+__global__ void __launch_bounds__(kFwdThreads, FwdRing<T, VL, NV>::kBlocks)
 norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma, const void *__restrict__ beta,
                      float eps, void *__restrict__ y, float *__restrict__ mean_out, float *__restrict__ invstd_out,
                      int64_t rows, int64_t C, int G, int S, int64_t per_block)
 {
-    using F = FwdRing<VL, NV>;
-    using R = RingItem<T, VL>;
-    constexpr int kRing = F::template stages<T>, eb = Store<T>::kBytes;
-    constexpr uint32_t kBytes = F::template bytes<T>;
+    using F = FwdRing<T, VL, NV>;
+    using V = RingView<T, VL>;
+    constexpr int kRing = F::stages, eb = Store<T>::kBytes;
+    constexpr uint32_t kBytes = F::bytes;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[kRing];
     __shared__ float red[2][2][8];
@@ -365,20 +444,17 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
     }
     __syncthreads();
     pdl_wait();
-    auto span = [&](int s, int64_t &first, uint32_t &n) {
+    auto fill = [&](int s, int st) {
         const int64_t a = r0 + (int64_t)s * S, b = a + S < r1 ? a + S : r1;
-        R::span(a * C, b * C, rows * C, first, n);
-    };
-    auto fill = [&](int s) {
         int64_t first;
         uint32_t n;
-        span(s, first, n);
-        const uint32_t bar = smem_addr(full + s % kRing);
+        V::span(a * C, b * C, rows * C, first, n);
+        const uint32_t bar = smem_addr(full + st);
         mbar_arrive_expect_tx(bar, n);
-        if (n) bulk_load(smem_addr(ring) + s % kRing * kBytes, static_cast<const unsigned char *>(x) + first * eb, n, bar);
+        if (n) bulk_load(smem_addr(ring) + st * kBytes, static_cast<const unsigned char *>(x) + first * eb, n, bar);
     };
     if (tid == 0)
-        for (int s = 0; s < kRing && s < steps; ++s) fill(s);
+        for (int s = 0; s < kRing && s < steps; ++s) fill(s, s);
 
     float wk[F::kKeep ? NV : 1][VL], bk[F::kKeep ? NV : 1][VL];
     int mine = 0;                                  // this thread's elements of a row
@@ -401,22 +477,23 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
         nl = lane < wpg ? red[0][0][w0 + lane] : 0.f;
         __syncthreads();
     }
+    V view(r0, r1, rows, C, S, slot, g, steps);
     int64_t row = r0 + slot;
-    for (int s = 0; s < steps; ++s, row += S) {
-        const int st = s % kRing;
-        if (!mbar_wait(smem_addr(full + st), (s / kRing) & 1)) atomicExch(&g_norm_error, 1u);
+    const int64_t at0 = (row * C + g * VL) * eb, hop = S * C * eb;
+    const unsigned char *xp = static_cast<const unsigned char *>(x) + at0;
+    unsigned char *yp = static_cast<unsigned char *>(y) + at0;
+    int st = 0;
+    uint32_t turn = 0;
+    for (int s = 0; s < steps; ++s, row += S, xp += hop, yp += hop) {
+        if (!mbar_wait(smem_addr(full + st), turn)) atomicExch(&g_norm_error, 1u);
         const bool live = row < r1;
         float h[NV][VL];
         float t[2] = {0.f, 0.f};
-        int64_t first;
-        uint32_t n;
-        span(s, first, n);
         if (live) {
-            const int skew = (int)(row * C - first);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 if (g + j * G < items) {
-                    R::load(ring + st * kBytes, n, skew, x, row * C, g + j * G, h[j]);
+                    view.load(ring + st * kBytes, s, xp, j * G, 0, h[j]);
                     if (RMS)
                         v_dot(h[j], h[j], t);
                     else
@@ -436,7 +513,7 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
                         float c[VL];
 #pragma unroll
                         for (int e = 0; e < VL; ++e) c[e] = h[j][e];
-                        v_center(c, mean, 1.f);
+                        v_shift(c, mean);
                         v_dot(c, c, t);
                     }
             }
@@ -447,22 +524,26 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
             red[s & 1][1][tid >> 5] = m2;
         }
         __syncthreads();                           // the rows' sums, and every thread has left the stage
-        if (tid == 0 && s + kRing < steps) fill(s + kRing);
+        if (tid == 0 && s + kRing < steps) fill(s + kRing, st);
+        if (++st == kRing) {
+            st = 0;
+            turn ^= 1;
+        }
+        view.next();
         if (G > 32) {
-            if constexpr (RMS) {
-                m2 = warps_sum(red[s & 1][1], w0, wpg);
-            } else {
+            const float qw = lane < wpg ? red[s & 1][1][w0 + lane] : 0.f;
+            float v = qw;
+            if constexpr (!RMS) {
                 const float mw = lane < wpg ? red[s & 1][0][w0 + lane] : 0.f;
-                const float qw = lane < wpg ? red[s & 1][1][w0 + lane] : 0.f;
-                float v = mw * nl;
+                float u = mw * nl;
 #pragma unroll
-                for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                mean = __shfl_sync(0xffffffffu, v, 0) * rc;
+                for (int off = 4; off >= 1; off >>= 1) u += __shfl_xor_sync(0xffffffffu, u, off);
+                mean = __shfl_sync(0xffffffffu, u, 0) * rc;
                 v = fmaf((mw - mean) * (mw - mean), nl, qw);
-#pragma unroll
-                for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                m2 = __shfl_sync(0xffffffffu, v, 0);
             }
+#pragma unroll
+            for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+            m2 = __shfl_sync(0xffffffffu, v, 0);
         }
         if (!live) continue;
         const float is = rsqrtf(fmaf(m2, rc, eps));
@@ -486,7 +567,7 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
                 }
                 v_center(h[j], mean, is);
                 v_fma(h[j], w, b);
-                Item<T, VL>::store(y, row * items + g + j * G, b);
+                Item<T, VL>::store(yp, j * G, b);
             }
     }
     pdl_trigger();
@@ -584,13 +665,15 @@ norm_cols_kernel(const void *__restrict__ x, const void *__restrict__ dy, const 
     }
 }
 
-// dgamma[c], dbeta[c]: the slabs' sums in order, in fp64.
+// dgamma[c], dbeta[c]: the slabs' sums in order, in fp64.  16 rows of threads
+// to 32 columns, eight loads in flight each.
+constexpr int kFinY = 16;
 template <typename TP>
-__global__ void __launch_bounds__(kColX *kColY)
+__global__ void __launch_bounds__(kColX *kFinY)
 norm_finish_kernel(const float *__restrict__ partial, void *__restrict__ dgamma, void *__restrict__ dbeta, int64_t C,
                    int64_t slabs)
 {
-    __shared__ double red[kColY][kColX];
+    __shared__ double red[kFinY][kColX];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * kColX + tx;   // over 2 C: dgamma, then dbeta
     const bool beta = i >= C;
@@ -598,51 +681,62 @@ norm_finish_kernel(const float *__restrict__ partial, void *__restrict__ dgamma,
     const bool live = i < 2 * C && out;
     pdl_wait();
     double s = 0.0;
-    if (live)
-        for (int64_t k = ty; k < slabs; k += kColY) s += partial[k * 2 * C + i];
+    if (live) {
+        const float *p = partial + i;
+        int64_t k = ty;
+        for (; k + 7 * kFinY < slabs; k += 8 * kFinY) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = p[(k + u * kFinY) * 2 * C];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
+        for (; k < slabs; k += kFinY) s += p[k * 2 * C];
+    }
     red[ty][tx] = s;
     __syncthreads();
     pdl_trigger();
     if (ty == 0 && live) {
 #pragma unroll
-        for (int k = 1; k < kColY; ++k) s += red[k][tx];
+        for (int k = 1; k < kFinY; ++k) s += red[k][tx];
         Store<TP>::store1(out, beta ? i - C : i, (float)s);
     }
 }
 
-// dx and the column sums of one slab of rows in one pass over x and dy.
-template <int VL, int NV>
+// The backward's ring: R rows of a thread between two barriers (32 elements,
+// 16 in fp32: a barrier, its waits and the shuffles of a row sum cost as much
+// as the arithmetic of 8), in stages of R S rows.
+template <typename T, int VL, int NV>
 struct BwdRing {
-    static constexpr int kThreads = 512;           // at most
-    static constexpr bool kKeep = VL * NV <= 8;    // gamma in registers (64 of them: two blocks per SM)
-    static constexpr int kBlocks = kKeep ? 2 : 1;
-    template <typename T>
-    static constexpr uint32_t bytes = (uint32_t)kThreads * NV * VL * Store<T>::kBytes + 32;   // of one tensor
-    template <typename T>
-    static constexpr int stages = (int)((kKeep ? 100u : 200u) * 1024 / (2 * bytes<T>)) < 8
-                                      ? (int)((kKeep ? 100u : 200u) * 1024 / (2 * bytes<T>))
-                                      : 8;
-    template <typename T>
-    static constexpr size_t smem = (size_t)stages<T> * 2 * bytes<T>;
+    static constexpr int kElems = 64 / Store<T>::kBytes;           // of a thread, per stage and tensor
+    static constexpr int R = VL * NV >= kElems ? 1 : kElems / (VL * NV) < 4 ? kElems / (VL * NV) : 4;
+    static constexpr bool kKeep = VL * NV <= 8;                    // gamma in registers
+    static constexpr uint32_t bytes = (uint32_t)kRingThreads * R * NV * VL * Store<T>::kBytes + 32;   // of one tensor
+    static constexpr int kFit = (int)((208u << 10) / (2 * bytes));
+    static constexpr int stages = kFit < 6 ? kFit : 6;
+    static constexpr size_t smem = (size_t)stages * 2 * bytes;
+    static_assert(stages >= 3, "a stage in use, one just left and one on its way");
 };
 
+// dx and the column sums of one slab of rows in one pass over x and dy: the
+// rows' sums, then the results, the elements read twice from the stage.
 template <typename T, typename TP, bool RMS, int VL, int NV>
-__global__ void __launch_bounds__(512, BwdRing<VL, NV>::kBlocks)
+__global__ void __launch_bounds__(kRingThreads, 1)
 norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gamma, const float *__restrict__ mean_in,
                      const float *__restrict__ invstd_in, void *dx, float *__restrict__ partial, int64_t rows,
                      int64_t C, int G, int S, int64_t per_slab)
 {
-    using F = BwdRing<VL, NV>;
-    using R = RingItem<T, VL>;
-    constexpr int kRing = F::template stages<T>, eb = Store<T>::kBytes;
-    constexpr uint32_t kBytes = F::template bytes<T>;
+    using F = BwdRing<T, VL, NV>;
+    using V = RingView<T, VL>;
+    constexpr int kRing = F::stages, eb = Store<T>::kBytes, R = F::R, N = RMS ? R : 2 * R;
+    constexpr uint32_t kBytes = F::bytes;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[kRing];
-    __shared__ float red[2][2][16];
-    const int tid = threadIdx.x, slot = tid / G, g = tid - slot * G, lb = lane_bits(G), wpg = G >> 5, w0 = slot * wpg;
-    const int items = (int)(C / VL);
+    __shared__ float red[2][N][16];
+    const int tid = threadIdx.x, slot = tid / G, g = tid - slot * G, w0 = slot * (G >> 5);
+    const int items = (int)(C / VL), SR = S * R;
     const int64_t r0 = (int64_t)blockIdx.x * per_slab, r1 = r0 + per_slab < rows ? r0 + per_slab : rows;
-    const int steps = r1 > r0 ? (int)((r1 - r0 + S - 1) / S) : 0;
+    const int steps = r1 > r0 ? (int)((r1 - r0 + SR - 1) / SR) : 0;
     const float rc = 1.f / (float)C;
     if (tid == 0) {
         for (int s = 0; s < kRing; ++s) mbar_init(smem_addr(full + s), 1);
@@ -650,15 +744,12 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
     }
     __syncthreads();
     pdl_wait();
-    auto span = [&](int s, int64_t &first, uint32_t &n) {
-        const int64_t a = r0 + (int64_t)s * S, b = a + S < r1 ? a + S : r1;
-        R::span(a * C, b * C, rows * C, first, n);
-    };
-    auto fill = [&](int s) {
+    auto fill = [&](int s, int st) {
+        const int64_t a = r0 + (int64_t)s * SR, b = a + SR < r1 ? a + SR : r1;
         int64_t first;
         uint32_t n;
-        span(s, first, n);
-        const uint32_t bar = smem_addr(full + s % kRing), dst = smem_addr(ring) + s % kRing * 2 * kBytes;
+        V::span(a * C, b * C, rows * C, first, n);
+        const uint32_t bar = smem_addr(full + st), dst = smem_addr(ring) + st * 2 * kBytes;
         mbar_arrive_expect_tx(bar, 2 * n);
         if (n) {
             bulk_load(dst, static_cast<const unsigned char *>(x) + first * eb, n, bar);
@@ -666,7 +757,7 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
         }
     };
     if (tid == 0)
-        for (int s = 0; s < kRing && s < steps; ++s) fill(s);
+        for (int s = 0; s < kRing && s < steps; ++s) fill(s, s);
 
     float wk[F::kKeep ? NV : 1][VL], ag[NV][VL], ab[NV][VL];
 #pragma unroll
@@ -685,69 +776,83 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
             v_mul(d, w, p);
         }
     };
+    V view(r0, r1, rows, C, SR, slot, g, steps);
+    const int row_hop = (int)(S * C);              // elements between a thread's rows of one stage
     int64_t row = r0 + slot;
-    float mean = 0.f, is = 0.f;
-    if (row < r1) {
-        if (!RMS) mean = mean_in[row];
-        is = invstd_in[row];
-    }
-    for (int s = 0; s < steps; ++s, row += S) {
-        const int st = s % kRing;
-        if (!mbar_wait(smem_addr(full + st), (s / kRing) & 1)) atomicExch(&g_norm_error, 1u);
-        const bool live = row < r1;
-        float mean_n = 0.f, is_n = 0.f;            // statistics of the next round
-        if (row + S < r1) {
-            if (!RMS) mean_n = mean_in[row + S];
-            is_n = invstd_in[row + S];
+    const int64_t at0 = (row * C + g * VL) * eb, hop = (int64_t)SR * C * eb, rh = (int64_t)row_hop * eb;
+    const unsigned char *xp = static_cast<const unsigned char *>(x) + at0;
+    const unsigned char *dp = static_cast<const unsigned char *>(dy) + at0;
+    unsigned char *op = static_cast<unsigned char *>(dx) + at0;
+    float mean_n[R], is_n[R];                      // statistics of the next stage's rows
+    auto stats = [&](int64_t from) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = from + r * S;
+            mean_n[r] = RMS || at >= r1 ? 0.f : mean_in[at];
+            is_n[r] = at >= r1 ? 0.f : invstd_in[at];
         }
-        float h[NV][VL], d[NV][VL];                // xhat, dy
-        float t1[2] = {0.f, 0.f}, t2[2] = {0.f, 0.f};
-        if (live) {
-            int64_t first;
-            uint32_t n;
-            span(s, first, n);
-            const int64_t base = row * C;
-            const int skew = (int)(base - first);
-            const unsigned char *sx = ring + st * 2 * kBytes;
+    };
+    stats(row);
+    int st = 0;
+    uint32_t turn = 0;
+    for (int s = 0; s < steps; ++s, row += SR, xp += hop, dp += hop, op += hop) {
+        float mean[R], is[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = mean_n[r];
+            is[r] = is_n[r];
+        }
+        if (!mbar_wait(smem_addr(full + st), turn)) atomicExch(&g_norm_error, 1u);
+        stats(row + SR);
+        const unsigned char *sx = ring + st * 2 * kBytes, *sd = sx + kBytes;
+        const int live = row < r1 ? (int)((r1 - row + S - 1) / S < R ? (r1 - row + S - 1) / S : R) : 0;   // this slot's rows
+        float v[N];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float t1[2] = {0.f, 0.f}, t2[2] = {0.f, 0.f};
+            if (r < live) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (g + j * G < items) {
+                        float h[VL], d[VL], p[VL];
+                        view.load(sx, s, xp + r * rh, j * G, r * row_hop, h);
+                        view.load(sd, s, dp + r * rh, j * G, r * row_hop, d);
+                        if (!RMS) v_shift(h, mean[r]);
+                        weigh(j, d, p);
+                        if (!RMS) v_sum(p, t1);
+                        v_dot(p, h, t2);
+                    }
+            }
+            v[r] = (t2[0] + t2[1]) * is[r];
+            if constexpr (!RMS) v[R + r] = t1[0] + t1[1];
+        }
+        reduce_rows<N>(v, G, w0, &red[s & 1]);
+        // every thread has left the stage before this one
+        const int prev = st == 0 ? kRing - 1 : st - 1;
+        if (tid == 0 && s > 0 && s - 1 + kRing < steps) fill(s - 1 + kRing, prev);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r >= live) break;
+            const float c1 = RMS ? 0.f : -is[r] * (v[N - R + r] * rc), c2 = -is[r] * (v[r] * rc);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 if (g + j * G < items) {
-                    R::load(sx, n, skew, x, base, g + j * G, h[j]);
-                    R::load(sx + kBytes, n, skew, dy, base, g + j * G, d[j]);
-                    float p[VL];
-                    v_center(h[j], mean, is);
-                    weigh(j, d[j], p);
-                    if (!RMS) v_sum(p, t1);
-                    v_dot(p, h[j], t2);
+                    float h[VL], d[VL], p[VL];
+                    view.load(sx, s, xp + r * rh, j * G, r * row_hop, h);
+                    view.load(sd, s, dp + r * rh, j * G, r * row_hop, d);
+                    v_center(h, mean[r], is[r]);
+                    v_fma(d, h, ag[j]);
+                    v_add(d, ab[j]);
+                    weigh(j, d, p);
+                    v_dx(p, h, is[r], c2, c1);
+                    Item<T, VL>::store(op + r * rh, j * G, p);
                 }
         }
-        float s1 = RMS ? 0.f : lanes_sum(t1[0] + t1[1], lb), s2 = lanes_sum(t2[0] + t2[1], lb);
-        // one barrier a round: the rows' sums are exchanged (in turn between
-        // two buffers), and every thread has left the stage
-        if (G > 32 && (tid & 31) == 0) {
-            red[s & 1][0][tid >> 5] = s1;
-            red[s & 1][1][tid >> 5] = s2;
+        if (++st == kRing) {
+            st = 0;
+            turn ^= 1;
         }
-        __syncthreads();
-        if (tid == 0 && s + kRing < steps) fill(s + kRing);
-        if (G > 32) {
-            if (!RMS) s1 = warps_sum(red[s & 1][0], w0, wpg);
-            s2 = warps_sum(red[s & 1][1], w0, wpg);
-        }
-        if (live) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (g + j * G < items) {
-                    float p[VL];
-                    v_fma(d[j], h[j], ag[j]);
-                    v_add(d[j], ab[j]);
-                    weigh(j, d[j], p);
-                    v_dx(p, h[j], s1 * rc, s2 * rc, is);
-                    Item<T, VL>::store(dx, row * items + g + j * G, p);
-                }
-        }
-        mean = mean_n;
-        is = is_n;
+        view.next();
     }
     pdl_trigger();
     if (!partial) return;
@@ -923,26 +1028,26 @@ cudaError_t by_nv(int nv, F f)
 template <typename T, typename TP, bool RMS, int VL, int NV>
 cudaError_t fwd_ring_nv(const NormLaunch &a, const RingGeo &r)
 {
-    using F = FwdRing<VL, NV>;
+    using F = FwdRing<T, VL, NV>;
     auto kernel = norm_fwd_ring_kernel<T, TP, RMS, VL, NV>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::template smem<T>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::smem);
     if (e != cudaSuccess) return e;
     int64_t blocks = (a.rows + r.S - 1) / r.S;
-    if (blocks > 148 * F::kBlocks) blocks = 148 * F::kBlocks;
+    if (blocks > F::kBlocks * sm_count()) blocks = F::kBlocks * sm_count();
     const int64_t per = (a.rows + blocks - 1) / blocks;
-    return launch_pdl(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(r.G * r.S), F::template smem<T>, a.stream,
-                      a.x, a.gamma, a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C, r.G, r.S, per);
+    return launch_pdl(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(r.G * r.S), F::smem, a.stream, a.x,
+                      a.gamma, a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C, r.G, r.S, per);
 }
 
-// The forward's ring: 16 elements of a row per thread, up to 64 (16 one by
-// one).  Few rows take the kernel above it: nothing to stream, and a row
-// spread over more threads answers sooner.
+// 16 elements of a row per thread, up to 64 (16 one by one) for rows of more
+// than 256 threads' worth.  Few rows take the kernel above it: nothing to
+// stream, and a row spread over more threads answers sooner.
 template <typename T, typename TP, bool RMS, int VL>
 bool fwd_ring(const NormLaunch &a, cudaError_t *e)
 {
-    constexpr int kWant = 16 / VL, kMost = VL == 1 ? 16 : VL == 4 ? 16 : 8;
+    constexpr int kWant = 16 / VL, kMost = VL == 1 ? 16 : 64 / VL;
     RingGeo r;
-    if (a.rows * a.C * Store<T>::kBytes < kRingBytes || !aligned16(a.x) || !ring_geo(a.C / VL, kWant, kMost, 256, &r))
+    if (a.rows * a.C * Store<T>::kBytes < kRingBytes || !aligned16(a.x) || !ring_geo(a.C / VL, kWant, kMost, kFwdThreads, &r))
         return false;
     *e = by_nv(r.nv, [&](auto n) -> cudaError_t {
         constexpr int NV = decltype(n)::value;
@@ -977,28 +1082,28 @@ cudaError_t fwd_vl(const NormLaunch &a)
 template <typename T, typename TP, bool RMS, int VL, int NV>
 cudaError_t bwd_ring_nv(const NormLaunch &a, const RingGeo &r)
 {
-    using F = BwdRing<VL, NV>;
+    using F = BwdRing<T, VL, NV>;
     auto kernel = norm_bwd_ring_kernel<T, TP, RMS, VL, NV>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::template smem<T>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::smem);
     if (e != cudaSuccess) return e;
     const bool sums = a.dgamma || a.dbeta;
-    const int64_t slabs = norm_slabs(a.rows, r.S), per = (a.rows + slabs - 1) / slabs;
-    e = launch_pdl(kernel, dim3((unsigned)slabs), dim3(r.G * r.S), F::template smem<T>, a.stream, a.x, a.dy, a.gamma,
+    const int64_t slabs = norm_slabs(a.rows, r.S * F::R), per = (a.rows + slabs - 1) / slabs;
+    e = launch_pdl(kernel, dim3((unsigned)slabs), dim3(r.G * r.S), F::smem, a.stream, a.x, a.dy, a.gamma,
                    a.mean_in, a.invstd_in, a.out, static_cast<float *>(sums ? a.workspace : nullptr), a.rows, a.C, r.G,
                    r.S, per);
     if (e != cudaSuccess || !sums) return e;
-    return launch_pdl(norm_finish_kernel<TP>, dim3((unsigned)((2 * a.C + kColX - 1) / kColX)), dim3(kColX * kColY), 0,
+    return launch_pdl(norm_finish_kernel<TP>, dim3((unsigned)((2 * a.C + kColX - 1) / kColX)), dim3(kColX * kFinY), 0,
                       a.stream, static_cast<const float *>(a.workspace), a.dgamma, a.dbeta, a.C, slabs);
 }
 
-// The backward's ring: 8 elements of a row per thread, up to 32 (16 one by
-// one) for rows of more than 512 threads' worth.
+// 8 elements of a row per thread, up to 32 (16 one by one) for rows of more
+// than 512 threads' worth.
 template <typename T, typename TP, bool RMS, int VL>
 bool bwd_ring(const NormLaunch &a, cudaError_t *e)
 {
-    constexpr int kWant = VL >= 8 ? 1 : 8 / VL, kMost = VL == 1 ? 16 : 32 / VL;
+    constexpr int kWant = 8 / VL, kMost = (VL == 1 ? 16 : Store<T>::kBytes == 2 ? 32 : 16) / VL;
     RingGeo r;
-    if (!aligned16(a.x) || !aligned16(a.dy) || !ring_geo(a.C / VL, kWant, kMost, 512, &r)) return false;
+    if (!aligned16(a.x) || !aligned16(a.dy) || !ring_geo(a.C / VL, kWant, kMost, kRingThreads, &r)) return false;
     *e = by_nv(r.nv, [&](auto n) -> cudaError_t {
         constexpr int NV = decltype(n)::value;
         if constexpr (NV > kMost)
@@ -1022,7 +1127,7 @@ cudaError_t bwd_vl(const NormLaunch &a)
                                    dim3(kColX * kColY), 0, a.stream, a.x, a.dy, a.mean_in, a.invstd_in, partial,
                                    a.rows, a.C, per, (unsigned)cb);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(norm_finish_kernel<TP>, dim3((unsigned)((2 * a.C + kColX - 1) / kColX)), dim3(kColX * kColY), 0,
+        e = launch_pdl(norm_finish_kernel<TP>, dim3((unsigned)((2 * a.C + kColX - 1) / kColX)), dim3(kColX * kFinY), 0,
                        a.stream, partial, a.dgamma, a.dbeta, a.C, slabs);
         if (e != cudaSuccess) return e;
     }
