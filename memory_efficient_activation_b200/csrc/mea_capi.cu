@@ -959,15 +959,16 @@ mea_status_t mea_norm_bwd(mea_norm_t norm, mea_dtype_t dtype, mea_dtype_t param_
 int mea_matmul_error_word(int clear)
 {
     clear_error();
-    unsigned int w = 0, wg = 0, wn = 0;
+    unsigned int w = 0, wg = 0, wf = 0, wn = 0;
     cudaError_t e = mea::matmul_error_word(clear, &w);
     if (e == cudaSuccess) e = mea::gated_error_word(clear, &wg);
+    if (e == cudaSuccess) e = mea::few_error_word(clear, &wf);
     if (e == cudaSuccess) e = mea::norm_error_word(clear, &wn);
     if (e != cudaSuccess) {
         cuda_fail(e, "mea_matmul_error_word");
         return -1;
     }
-    return (int)(w | wg | wn);
+    return (int)(w | wg | wf | wn);
 }
 
 static mea_status_t bn_common(const char *name, int dtype, int npieces, const void *const *pieces,

@@ -57,6 +57,7 @@ constexpr int kAcc = 256;                                   // accumulator colum
 constexpr int kBK = 64;                                     // K per pipeline stage: 128 bytes
 constexpr int kHalf = 128;                                  // rows (columns) of A and B one CTA stages
 constexpr int kUmmaK = 16;
+constexpr int kFewMax = kFewTokens;                         // tokens up to which launch_few serves
 constexpr int kGroupM = 8;                                  // row tiles per group of the tile order
 constexpr uint32_t kStageA = kHalf * kBK * 2;               // 16 KB
 constexpr uint32_t kStageBytes = 2 * kStageA;
@@ -686,7 +687,11 @@ cudaError_t gated_error_word(int clear, unsigned int *word)
     return e;
 }
 
-cudaError_t launch_gated(const GatedLaunch &a) { return a.mode == 0 ? by_act<kFwd>(a) : by_act<kBwd>(a); }
+cudaError_t launch_gated(const GatedLaunch &a)
+{
+    if (a.mode == 1) return by_act<kBwd>(a);
+    return a.M <= kFewMax ? launch_few(a, true) : by_act<kFwd>(a);
+}
 
 cudaError_t launch_matmul(const MatmulPlain &p)
 {
@@ -699,7 +704,8 @@ cudaError_t launch_matmul(const MatmulPlain &p)
     a.z = p.c;
     a.stream = p.stream;
     if (p.trans_a) return launch_one<ReLU, kPlainTN>(a);
-    return p.trans_b ? launch_one<ReLU, kPlainNT>(a) : launch_one<ReLU, kPlainNN>(a);
+    if (p.trans_b) return a.M <= kFewMax ? launch_few(a, false) : launch_one<ReLU, kPlainNT>(a);
+    return launch_one<ReLU, kPlainNN>(a);
 }
 
 }  // namespace mea

@@ -41,6 +41,11 @@ struct MatmulPlain {
     cudaStream_t stream;
 };
 
+// Few tokens: the forward's (gated) or a plain product with a [N x K] weight
+// (x = A, w0 = B, z = C), M at most kFewTokens.
+constexpr int kFewTokens = 256;
+cudaError_t launch_few(const GatedLaunch &a, bool gated);
+cudaError_t few_error_word(int clear, unsigned int *word);     // synchronous
 cudaError_t launch_matmul(const MatmulPlain &p);
 cudaError_t launch_gated(const GatedLaunch &a);
 cudaError_t gated_error_word(int clear, unsigned int *word);   // synchronous
