@@ -108,7 +108,14 @@ def _shaped(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     return t
 
 
+# The handle of a device's current stream without building a Stream object (3
+# us of a small call's host time), where this PyTorch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -651,22 +658,24 @@ def _norm_id(norm: str) -> int:
         raise ValueError(f"unknown norm {norm!r}; one of {tuple(NORM_IDS)}") from None
 
 
-def _norm_args(x: torch.Tensor, params) -> tuple:
+def _norm_args(x: torch.Tensor, gamma, beta) -> tuple:
     """Checks a normalised tensor and its per-channel parameters (None or
-    contiguous [C], all of one dtype); returns (rows, C, parameter dtype)."""
+    contiguous [C] of one dtype); returns (rows, C, ids of both dtypes)."""
     _need_cuda(x)
-    _dtype_id(x)
-    if x.dim() < 1 or x.shape[-1] == 0:
+    did = _dtype_id(x)
+    C = x.shape[-1] if x.dim() else 0
+    if C == 0:
         raise ValueError("x needs a last dimension of at least one element to normalise over")
-    C = x.shape[-1]
-    pdt = None
-    for name, t in params:
+    pid = None
+    for name, t in (("gamma", gamma), ("beta", beta)):
         if t is None:
             continue
-        _dtype_id(t)
-        _shaped(t, (C,), t.dtype if pdt is None else pdt, x.device, name)
-        pdt = t.dtype
-    return x.numel() // C, C, pdt or torch.float32
+        _need_cuda(t)
+        tid = _dtype_id(t)
+        if t.dim() != 1 or t.shape[0] != C or t.device != x.device or (pid is not None and tid != pid):
+            raise ValueError(f"{name} must be a contiguous [{C}] tensor on {x.device}, gamma and beta of one dtype")
+        pid = tid
+    return x.numel() // C, C, did, _capi.MEA_F32 if pid is None else pid
 
 
 def norm_fwd(norm: str, x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -676,11 +685,14 @@ def norm_fwd(norm: str, x: torch.Tensor, gamma: torch.Tensor | None = None, beta
     shape (mean None for "rms", both None without want_stats).  gamma, beta:
     [C] in fp32 or bf16 (one dtype for both), None for 1 and 0."""
     kind = _norm_id(norm)
-    rows, C, pdt = _norm_args(x, (("gamma", gamma), ("beta", beta)))
+    rows, C, did, pid = _norm_args(x, gamma, beta)
     y = torch.empty_like(x) if out is None else _like(x, out, "out")
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_stats and norm == "layer" else None
-    invstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_stats else None
-    _call("mea_norm_fwd", x, kind, _dtype_id(x), _DTYPES[pdt], rows, C, x.data_ptr(), _ptr(gamma), _ptr(beta),
+    mean = invstd = None
+    if want_stats:
+        invstd = x.new_empty(rows if x.dim() == 2 else x.shape[:-1], dtype=torch.float32)
+        if norm == "layer":
+            mean = torch.empty_like(invstd)
+    _call("mea_norm_fwd", x, kind, did, pid, rows, C, x.data_ptr(), _ptr(gamma), _ptr(beta),
           float(eps), y.data_ptr(), _ptr(mean), _ptr(invstd))
     return y, mean, invstd
 
@@ -699,7 +711,7 @@ def norm_bwd(norm: str, x: torch.Tensor, dy: torch.Tensor, gamma: torch.Tensor |
     bytes of any contents; allocated per call when not given, so that calls on
     several streams or captured in several graphs never share one."""
     kind = _norm_id(norm)
-    rows, C, pdt = _norm_args(x, (("gamma", gamma),))
+    rows, C, did, pid = _norm_args(x, gamma, None)
     if dy.dtype != x.dtype or dy.shape != x.shape:
         raise ValueError("dy must match x in dtype and shape")
     _like(x, dy, "dy")
@@ -711,15 +723,16 @@ def norm_bwd(norm: str, x: torch.Tensor, dy: torch.Tensor, gamma: torch.Tensor |
     if want_dgamma is None:
         want_dgamma = gamma is not None
     dx = torch.empty_like(x) if out is None else _like(x, out, "out")
-    dgamma = torch.empty(C, dtype=pdt, device=x.device) if want_dgamma else None
-    dbeta = torch.empty(C, dtype=pdt, device=x.device) if want_dbeta else None
+    pdt = torch.float32 if gamma is None else gamma.dtype
+    dgamma = x.new_empty(C, dtype=pdt) if want_dgamma else None
+    dbeta = x.new_empty(C, dtype=pdt) if want_dbeta else None
     ws_ptr, ws_bytes = None, 0
     if want_dgamma or want_dbeta:
         if workspace is None:
-            workspace = torch.empty(norm_bwd_workspace_bytes(rows, C), dtype=torch.uint8, device=x.device)
+            workspace = x.new_empty(norm_bwd_workspace_bytes(rows, C), dtype=torch.uint8)
         _on_device(x, workspace, "workspace")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call("mea_norm_bwd", x, kind, _dtype_id(x), _DTYPES[pdt], rows, C, x.data_ptr(), dy.data_ptr(), _ptr(gamma),
+    _call("mea_norm_bwd", x, kind, did, pid, rows, C, x.data_ptr(), dy.data_ptr(), _ptr(gamma),
           _ptr(mean) if norm == "layer" else None, invstd.data_ptr(), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
           ws_ptr, ws_bytes)
     return dx, dgamma, dbeta
