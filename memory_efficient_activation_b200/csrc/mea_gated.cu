@@ -78,11 +78,11 @@ struct Shape {
     // us against 196).
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 64 + 32 * kWarps;
-    // Chunk buffers per warp.  Backward: gate and up as they arrive (read into
-    // registers at once, so that the next chunk's loads fly during this one's
-    // arithmetic), dgate, dup and h.  Forward: gate, up and h.  Plain: two of
-    // C in turn.
-    static constexpr int kChunks = MODE == kBwd ? 5 : MODE == kFwd ? 3 : 2;
+    // Chunk buffers per warp.  Backward: gate and up as they arrive, of two
+    // chunks (read into registers at once, so that two more are on their way
+    // during the arithmetic: 32 KB in flight per SM), dgate, dup and h.
+    // Forward: gate, up and h.  Plain: two of C in turn.
+    static constexpr int kChunks = MODE == kBwd ? 7 : MODE == kFwd ? 3 : 2;
     static constexpr uint32_t kEpiBytes = kWarps * kChunks * kChunk;
     // Pipeline stages: what is left of the shared memory.
     static constexpr int kStages = MODE == kBwd ? 5 : 6;
@@ -364,8 +364,8 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
     uint64_t *empty = full + kStages;
     uint64_t *acc_full = empty + kStages;
     uint64_t *acc_empty = acc_full + 2;
-    uint64_t *in_full = acc_empty + 2;                     // backward: a chunk of z has landed, per warp
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(in_full + S::kWarps);
+    uint64_t *in_full = acc_empty + 2;                     // backward: a chunk of z has landed, two per warp
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(in_full + 2 * S::kWarps);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();          // 0: issues the MMAs of the pair
@@ -383,7 +383,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
             mbar_init(smem_addr(acc_full + b), 1);
             mbar_init(smem_addr(acc_empty + b), 2 * S::kWarps);   // the epilogue warps of both CTAs
         }
-        for (int i = 0; i < S::kWarps; ++i) mbar_init(smem_addr(in_full + i), 1);
+        for (int i = 0; i < 2 * S::kWarps; ++i) mbar_init(smem_addr(in_full + i), 1);
         mbar_init_fence();
     }
     if (warp == 1) {
@@ -488,34 +488,55 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
         const uint32_t mine = ebase + ew * (S::kChunks * kChunk);
         constexpr int kHalves = S::kWarps / 4, kMost = kTN / 32 / kHalves;   // column shares, chunks of one
         const int c0 = (ew >> 2) * kMost;                  // this warp's first chunk
-        const uint32_t in_bar = smem_addr(in_full + ew);
+        const uint32_t in_bars = smem_addr(in_full + 2 * ew);
         const int row_in = (int)rank * kHalf + q * 32;
-        // chunks of tile t with something in them, from c0 on
-        auto chunks = [&](int t) {
+        // Where this warp's chunks of tile t lie, and how many have something
+        // in them.  Its divisions are done once per tile: once per chunk they
+        // took as long as the arithmetic.
+        struct Place {
+            int row, col, nc;
+        };
+        auto place = [&](int t) {
             int tm, tn;
             tile_of(t, tiles_m, tiles_n, tm, tn);
-            if (tm * kBM + row_in >= M) return 0;
-            const int left = (N - tn * kTN + 31) / 32 - c0;
-            return left < 0 ? 0 : left < kMost ? left : kMost;
+            Place p;
+            p.row = tm * kBM + row_in;
+            p.col = tn * kTN + c0 * 32;
+            const int left = (N - p.col + 31) / 32;
+            p.nc = p.row >= M || left < 0 ? 0 : left < kMost ? left : kMost;
+            return p;
         };
-        auto fetch = [&](int t, int c) {                   // backward: z of a chunk
+        // backward: z of chunk fc of the tile at fp (the ft-th), the next one
+        // to fetch; fetched counts those asked for
+        int ft = pair, fc = 0, fetched = 0;
+        Place fp = place(ft);
+        auto seek = [&] {                                  // the next tile with chunks
+            while (ft < ntiles && fp.nc == 0) {
+                ft += npairs;
+                if (ft < ntiles) fp = place(ft);
+            }
+        };
+        auto fetch = [&] {
+            if (ft >= ntiles) return;
             if (lane == 0) {
-                int tm, tn;
-                tile_of(t, tiles_m, tiles_n, tm, tn);
-                const int col = tn * kTN + (c0 + c) * 32, row = tm * kBM + row_in;
-                mbar_arrive_expect_tx(in_bar, 2 * kChunk);
-                chunk_load(mine, &maps.in0, col, row, in_bar);
-                chunk_load(mine + kChunk, &maps.in1, col, row, in_bar);
+                const uint32_t dst = mine + (fetched & 1) * 2 * kChunk, bar = in_bars + 8 * (fetched & 1);
+                mbar_arrive_expect_tx(bar, 2 * kChunk);
+                chunk_load(dst, &maps.in0, fp.col + fc * 32, fp.row, bar);
+                chunk_load(dst + kChunk, &maps.in1, fp.col + fc * 32, fp.row, bar);
+            }
+            ++fetched;
+            if (++fc == fp.nc) {
+                fc = 0;
+                fp.nc = 0;
+                seek();
             }
         };
         int n = 0;                                         // chunks taken so far
-        bool ok = true, ahead = false;                     // ahead: chunk n is on its way
+        bool ok = true;
         if constexpr (MODE == kBwd) {
-            for (int t = pair; t < ntiles && !ahead; t += npairs)
-                if (chunks(t) > 0) {
-                    fetch(t, 0);
-                    ahead = true;
-                }
+            seek();
+            fetch();
+            fetch();
         }
         int lt = 0;
         for (int t = pair; t < ntiles; t += npairs, ++lt) {
@@ -526,16 +547,14 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
             }
             if (!ok) break;
             tc_fence_after();
-            int tm, tn;
-            tile_of(t, tiles_m, tiles_n, tm, tn);
+            const Place p = place(t);
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + b * kAcc;
-            const int row = tm * kBM + row_in, nc = chunks(t);
 #pragma unroll 1
-            for (int c = 0; c < nc; ++c, ++n) {
+            for (int c = 0; c < p.nc; ++c, ++n) {
                 uint32_t v[32], w[16];
                 tmem_ld32(lanes + (c0 + c) * 32, v);
-                const int col = tn * kTN + (c0 + c) * 32;
-                const uint32_t buf = mine + (MODE == kBwd ? 2 : MODE == kFwd ? 0 : n & 1) * kChunk;
+                const int row = p.row, col = p.col + c * 32;
+                const uint32_t buf = mine + (MODE == kBwd ? 4 : MODE == kFwd ? 0 : n & 1) * kChunk;
                 if constexpr (MODE == kFwd) {
                     uint32_t u[32];
                     tmem_ld32(lanes + kHalf + (c0 + c) * 32, u);
@@ -553,25 +572,16 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                     }
                 } else if constexpr (MODE == kBwd) {
                     uint32_t uw[16], hw[16];
-                    ahead = false;
-                    if (!mbar_wait(in_bar, n & 1)) {
+                    const uint32_t in = mine + (n & 1) * 2 * kChunk;
+                    if (!mbar_wait(in_bars + 8 * (n & 1), (n >> 1) & 1)) {
                         record_error();
                         ok = false;
                         break;
                     }
-                    load_row(mine, lane, w);
-                    load_row(mine + kChunk, lane, uw);
+                    load_row(in, lane, w);
+                    load_row(in + kChunk, lane, uw);
                     __syncwarp();
-                    int nt = t, nx = c + 1;                // the next chunk's z
-                    if (nx == nc) {
-                        nx = 0;
-                        do nt += npairs;
-                        while (nt < ntiles && chunks(nt) == 0);
-                    }
-                    if (nt < ntiles) {
-                        fetch(nt, nx);
-                        ahead = true;
-                    }
+                    fetch();
                     product_bwd<A>(v, k, w, uw, hw);
                     if (lane == 0) store_wait_read<0>();   // of the chunk before: long done
                     __syncwarp();
@@ -601,7 +611,8 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
             if (lane == 0) mbar_arrive_cluster(release + 8 * b);
         }
         // what is in flight has landed before this CTA's memory goes away
-        if (ahead && !mbar_wait(in_bar, n & 1)) record_error();
+        for (; n < fetched; ++n)
+            if (!mbar_wait(in_bars + 8 * (n & 1), (n >> 1) & 1)) record_error();
         if (lane == 0) store_wait_read<0>();
     }
     pdl_trigger();
