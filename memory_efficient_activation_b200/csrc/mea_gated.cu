@@ -57,7 +57,6 @@ constexpr int kAcc = 256;                                   // accumulator colum
 constexpr int kBK = 64;                                     // K per pipeline stage: 128 bytes
 constexpr int kHalf = 128;                                  // rows (columns) of A and B one CTA stages
 constexpr int kUmmaK = 16;
-constexpr int kFewMax = kFewTokens;                         // tokens up to which launch_few serves
 constexpr int kGroupM = 8;                                  // row tiles per group of the tile order
 constexpr uint32_t kStageA = kHalf * kBK * 2;               // 16 KB
 constexpr uint32_t kStageBytes = 2 * kStageA;
@@ -81,11 +80,14 @@ struct Shape {
     // Chunk buffers per warp.  Backward: gate and up as they arrive, of two
     // chunks (read into registers at once, so that two more are on their way
     // during the arithmetic: 32 KB in flight per SM), dgate, dup and h.
-    // Forward: gate, up and h.  Plain: two of C in turn.
-    static constexpr int kChunks = MODE == kBwd ? 7 : MODE == kFwd ? 3 : 2;
+    // Forward: gate, up and h, plain: C, kOut sets of them in turn: a store
+    // reads its chunk some 1000 cycles after it was issued, which one set
+    // would wait for every time.
+    static constexpr int kOut = MODE == kBwd ? 1 : MODE == kFwd ? 2 : 4;
+    static constexpr int kChunks = MODE == kBwd ? 7 : MODE == kFwd ? 3 * kOut : kOut;
     static constexpr uint32_t kEpiBytes = kWarps * kChunks * kChunk;
     // Pipeline stages: what is left of the shared memory.
-    static constexpr int kStages = MODE == kBwd ? 5 : 6;
+    static constexpr int kStages = MODE == kBwd || MODE == kFwd ? 5 : 6;
     static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiBytes + 256;
     static_assert(kSmemBytes <= 232448, "shared memory of a block");
 };
@@ -374,6 +376,20 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
     const int ntiles = tiles_m * tiles_n;
     const int kblocks = (K + kBK - 1) / kBK;
 
+    if (threadIdx.x == 32) {                       // descriptors on their way while the barriers are set up
+        prefetch_map(&maps.x);
+        prefetch_map(&maps.w0);
+        if constexpr (MODE == kFwd) prefetch_map(&maps.w1);
+        if constexpr (MODE == kBwd) {
+            prefetch_map(&maps.in0);
+            prefetch_map(&maps.in1);
+        }
+        if (MODE != kFwd || want01) prefetch_map(&maps.out0);
+        if constexpr (MODE == kFwd || MODE == kBwd) {
+            if (want01) prefetch_map(&maps.out1);
+            if (want2) prefetch_map(&maps.out2);
+        }
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_addr(full + s), 1);     // the first CTA's producer; bytes of both CTAs
@@ -554,11 +570,11 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                 uint32_t v[32], w[16];
                 tmem_ld32(lanes + (c0 + c) * 32, v);
                 const int row = p.row, col = p.col + c * 32;
-                const uint32_t buf = mine + (MODE == kBwd ? 4 : MODE == kFwd ? 0 : n & 1) * kChunk;
+                const uint32_t buf = mine + (MODE == kBwd ? 4 : n % S::kOut * (MODE == kFwd ? 3 : 1)) * kChunk;
                 if constexpr (MODE == kFwd) {
                     uint32_t u[32];
                     tmem_ld32(lanes + kHalf + (c0 + c) * 32, u);
-                    if (lane == 0) store_wait_read<0>();
+                    if (lane == 0) store_wait_read<S::kOut - 1>();
                     __syncwarp();
                     if (want01) {
                         pack32(v, w);
@@ -590,7 +606,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                     if (want2) store_row(buf + 2 * kChunk, lane, hw);
                 } else {
                     pack32(v, w);
-                    if (lane == 0) store_wait_read<1>();
+                    if (lane == 0) store_wait_read<S::kOut - 1>();
                     __syncwarp();
                     store_row(buf, lane, w);
                 }
@@ -698,10 +714,22 @@ cudaError_t gated_error_word(int clear, unsigned int *word)
     return e;
 }
 
+// Whether the few-token kernel serves M rows with `tiles` column tiles of this
+// kernel.  Up to 64 rows always: this kernel would multiply mostly zeros.
+// Beyond, while the tiles leave pairs of SMs idle that shares of K use: all
+// of them at 65-128 rows, half at 129-256 (K 4096, us, few tokens / this
+// kernel: 64 tiles, M 128 41.8 / 43.9 and 256 50.1 / 43.8; 32 tiles, M 256
+// 32.9 / 36.9; 128 tiles, M 64 63.5 / 69.6 and 128 72.7 / 69.6).
+bool few_tokens(int64_t M, int64_t tiles)
+{
+    const int64_t pairs = sm_count() / 2;
+    return M <= 64 || (M <= 128 && tiles <= pairs) || (M <= kFewTokens && 2 * tiles <= pairs);
+}
+
 cudaError_t launch_gated(const GatedLaunch &a)
 {
     if (a.mode == 1) return by_act<kBwd>(a);
-    return a.M <= kFewMax ? launch_few(a, true) : by_act<kFwd>(a);
+    return few_tokens(a.M, (a.N + kHalf - 1) / kHalf) ? launch_few(a, true) : by_act<kFwd>(a);
 }
 
 cudaError_t launch_matmul(const MatmulPlain &p)
@@ -715,7 +743,8 @@ cudaError_t launch_matmul(const MatmulPlain &p)
     a.z = p.c;
     a.stream = p.stream;
     if (p.trans_a) return launch_one<ReLU, kPlainTN>(a);
-    if (p.trans_b) return a.M <= kFewMax ? launch_few(a, false) : launch_one<ReLU, kPlainNT>(a);
+    if (p.trans_b)
+        return few_tokens(a.M, (a.N + kAcc - 1) / kAcc) ? launch_few(a, false) : launch_one<ReLU, kPlainNT>(a);
     return launch_one<ReLU, kPlainNN>(a);
 }
 

@@ -117,6 +117,11 @@ few_kernel(const __grid_constant__ FewArgs a)
     const int kb0 = (int)((int64_t)kb_all * rank / KS), kbs = (int)((int64_t)kb_all * (rank + 1) / KS) - kb0;
     const uint32_t stage_bytes = kBytesW + (uint32_t)a.mt * (kBK * 2);
 
+    if (threadIdx.x == 32) {
+        prefetch_map(&a.x);
+        prefetch_map(&a.w0);
+        if (kGated) prefetch_map(&a.w1);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(smem_addr(full + s), 1);

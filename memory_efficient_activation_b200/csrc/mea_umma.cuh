@@ -36,6 +36,12 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// Brings a tensor map into the descriptor cache ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // shared::cluster address of the variable at `saddr` in CTA `rank` of the
 // cluster.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank)
