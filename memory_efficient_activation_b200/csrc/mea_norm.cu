@@ -573,6 +573,122 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
     pdl_trigger();
 }
 
+// Forward with a warp to a row: 8 warps of a block, two blocks per SM, take
+// rows in turn.  A warp holds its row in registers (NV vectors a lane, all of
+// their loads in flight at once), sums by shuffles alone and meets no barrier;
+// gamma and beta wait in shared memory, where reading them costs no latency
+// of L1 and no registers.  Half the instructions of the ring's.
+constexpr int kWarpThreads = 256;
+template <typename T, typename TP, bool RMS, int NV>
+__global__ void __launch_bounds__(kWarpThreads, 2)
+norm_fwd_warp_kernel(const void *__restrict__ x, const void *__restrict__ gamma, const void *__restrict__ beta,
+                     float eps, void *__restrict__ y, float *__restrict__ mean_out, float *__restrict__ invstd_out,
+                     int64_t rows, int64_t C)
+{
+    constexpr int VL = Store<T>::V;
+    // 16-byte words of VL parameters; words apart, so that a warp reads each
+    // in one piece
+    constexpr int kWords = VL * Store<TP>::kBytes >= 16 ? VL * Store<TP>::kBytes / 16 : 1;
+    constexpr bool kHalf = VL * Store<TP>::kBytes < 16;      // four bf16 beside four fp32: 8 bytes
+    extern __shared__ uint4 par[];
+    const int items = (int)(C / VL), lane = threadIdx.x & 31;
+    const float rc = 1.f / (float)C;
+    pdl_wait();
+    uint4 *sg = par, *sb = par + kWords * items;
+    for (int i = threadIdx.x; i < items; i += kWarpThreads) {
+        float w[VL], b[VL];
+        load_params<TP, VL>(gamma, i, 1.f, w);
+        load_params<TP, VL>(beta, i, 0.f, b);
+        if constexpr (kHalf) {
+            sg[i] = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(b[0], b[1]),
+                               pack_bf16x2(b[2], b[3]));
+        } else {
+            constexpr int PV = Store<TP>::V;
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                float t[PV], u[PV];
+#pragma unroll
+                for (int e = 0; e < PV; ++e) {
+                    t[e] = w[k * PV + e];
+                    u[e] = b[k * PV + e];
+                }
+                sg[k * items + i] = Store<TP>::pack(t);
+                sb[k * items + i] = Store<TP>::pack(u);
+            }
+        }
+    }
+    __syncthreads();
+    auto params = [&](int i, float (&w)[VL], float (&b)[VL]) {
+        if constexpr (kHalf) {
+            float t[8];
+            Store<Bf16>::unpack(sg[i], t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = t[e];
+                b[e] = t[4 + e];
+            }
+        } else {
+            constexpr int PV = Store<TP>::V;
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                float t[PV], u[PV];
+                Store<TP>::unpack(sg[k * items + i], t);
+                Store<TP>::unpack(sb[k * items + i], u);
+#pragma unroll
+                for (int e = 0; e < PV; ++e) {
+                    w[k * PV + e] = t[e];
+                    b[k * PV + e] = u[e];
+                }
+            }
+        }
+    };
+    constexpr int kWarps = kWarpThreads / 32;
+    for (int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * kWarps) {
+        const uint4 *xr = static_cast<const uint4 *>(x) + row * items + lane;
+        uint4 *yr = static_cast<uint4 *>(y) + row * items + lane;
+        uint4 r[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane + 32 * j < items) r[j] = ld_nc_v4(xr + 32 * j);
+        float mean = 0.f, t[2] = {0.f, 0.f};
+        if constexpr (!RMS) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (lane + 32 * j < items) {
+                    float f[VL];
+                    Store<T>::unpack(r[j], f);
+                    v_sum(f, t);
+                }
+            mean = lanes_sum(t[0] + t[1], 5) * rc;
+            t[0] = t[1] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane + 32 * j < items) {
+                float f[VL];
+                Store<T>::unpack(r[j], f);
+                if (!RMS) v_shift(f, mean);
+                v_dot(f, f, t);
+            }
+        const float is = rsqrtf(fmaf(lanes_sum(t[0] + t[1], 5), rc, eps));
+        if (lane == 0) {
+            if (!RMS && mean_out) mean_out[row] = mean;
+            if (invstd_out) invstd_out[row] = is;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane + 32 * j < items) {
+                float f[VL], w[VL], b[VL];
+                Store<T>::unpack(r[j], f);
+                params(lane + 32 * j, w, b);
+                v_center(f, mean, is);
+                v_fma(f, w, b);
+                st_v4(yr + 32 * j, Store<T>::pack(b));
+            }
+    }
+    pdl_trigger();
+}
+
 // Rows too long for the registers of a block: one block per row, which is
 // read again for each of the passes.
 template <typename T, typename TP, bool RMS>
@@ -1059,10 +1175,35 @@ bool fwd_ring(const NormLaunch &a, cudaError_t *e)
     return true;
 }
 
+// The warp-to-a-row forward: rows of 33 to 512 vectors (below, lanes idle or
+// shuffles outweigh the row), and enough of them to give every warp some.
+template <typename T, typename TP, bool RMS>
+bool fwd_warp(const NormLaunch &a, cudaError_t *e)
+{
+    const int64_t items = a.C / Store<T>::V, grid = 2 * sm_count();
+    if (items <= 32 || items > 512 || a.rows < grid * (kWarpThreads / 32)) return false;
+    constexpr int kParam = Store<T>::V * Store<TP>::kBytes * 2 < 16 ? 16 : Store<T>::V * Store<TP>::kBytes * 2;
+    int nv = 2;
+    while (nv * 32 < items) nv <<= 1;
+    *e = by_nv(nv, [&](auto n) -> cudaError_t {
+        auto kernel = norm_fwd_warp_kernel<T, TP, RMS, decltype(n)::value>;
+        const size_t smem = (size_t)items * kParam;
+        if (smem > 48 * 1024) {
+            cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (s != cudaSuccess) return s;
+        }
+        return launch_pdl(kernel, dim3((unsigned)grid), dim3(kWarpThreads), smem, a.stream, a.x, a.gamma, a.beta, a.eps,
+                          a.out, a.mean, a.invstd, a.rows, a.C);
+    });
+    return true;
+}
+
 template <typename T, typename TP, bool RMS, int VL>
 cudaError_t fwd_vl(const NormLaunch &a)
 {
     cudaError_t re;
+    if constexpr (VL > 1)
+        if (fwd_warp<T, TP, RMS>(a, &re)) return re;
     if (fwd_ring<T, TP, RMS, VL>(a, &re)) return re;
     const Group g = pick_group(a.C / VL, a.rows, 16);
     if (g.nv == 0)
