@@ -230,52 +230,48 @@ struct RingGeo {
     int G, S, nv;            // threads to a row, rows at a time, items per thread
 };
 
-// A thread's view of the stages: where its items lie, step by step.
+// The copy of a stage and a thread's view of it.
 template <typename T, int VL>
 struct RingView {
     static constexpr int q = 16 / Store<T>::kBytes;
-    // First element and bytes of the copy for elements [a, b) of a tensor of
-    // `end` elements.
-    static __device__ __forceinline__ void span(int64_t a, int64_t b, int64_t end, int64_t &first, uint32_t &n)
+    // Elements [a, b) of a tensor of `end` elements into the stage at dst:
+    // the bytes of the bulk copy, which starts on the boundary at or before a.
+    // One thread calls this; the copy completes on `bar`, the few elements
+    // that a copy to the boundary after the tensor's end would overrun are
+    // stored here (a barrier of the block comes between that and their use).
+    static __device__ __forceinline__ uint32_t bytes(int64_t a, int64_t b, int64_t end)
     {
-        first = a & ~(int64_t)(q - 1);
         const int64_t up = (b + q - 1) & ~(int64_t)(q - 1);
-        n = (uint32_t)(((up <= end ? up : b & ~(int64_t)(q - 1)) - first) * Store<T>::kBytes);
+        return (uint32_t)(((up <= end ? up : b & ~(int64_t)(q - 1)) - (a & ~(int64_t)(q - 1))) * Store<T>::kBytes);
+    }
+    static __device__ __forceinline__ void copy(unsigned char *dst, const void *p, int64_t a, int64_t b, uint32_t n,
+                                                uint32_t bar)
+    {
+        const int64_t first = a & ~(int64_t)(q - 1);
+        if (n) bulk_load(smem_addr(dst), static_cast<const unsigned char *>(p) + first * Store<T>::kBytes, n, bar);
+        if constexpr (VL == 1)
+            for (int64_t i = first + n / Store<T>::kBytes; i < b; ++i) Store<T>::store1(dst, i - first, load1_rw<T>(p, i));
     }
     uint32_t at;             // this thread's item 0: elements from the rows' start in the stage
     uint32_t skew, turn;     // VL 1: elements before the rows' start, and their change per step
-    uint32_t last, n_last;   // VL 1: the step whose copy ends short of its rows, and its bytes
-    __device__ __forceinline__ RingView(int64_t r0, int64_t r1, int64_t rows, int64_t C, int per, int slot, int g, int steps)
+    __device__ __forceinline__ RingView(int64_t r0, int64_t C, int per, int slot, int g)
     {
         at = (uint32_t)(slot * C) + g * VL;
-        skew = turn = n_last = 0;
-        last = 0xffffffffu;
-        if constexpr (VL == 1) {
-            skew = (uint32_t)((r0 * C) & (q - 1));
-            turn = (uint32_t)((per * C) & (q - 1));
-            if (r1 == rows && steps > 0) {
-                int64_t first;
-                last = steps - 1;
-                span((r0 + (int64_t)last * per) * C, r1 * C, rows * C, first, n_last);
-            }
-        }
+        skew = VL == 1 ? (uint32_t)((r0 * C) & (q - 1)) : 0u;
+        turn = VL == 1 ? (uint32_t)((per * C) & (q - 1)) : 0u;
     }
     __device__ __forceinline__ void next()
     {
         if constexpr (VL == 1) skew = (skew + turn) & (q - 1);
     }
     // The i-th item after item 0 in the row that starts `off` elements after
-    // this thread's first, from the stage; p is the tensor at item 0 of that
-    // row.
-    __device__ __forceinline__ void load(const unsigned char *stage, int s, const void *p, int i, int off,
-                                         float (&f)[VL]) const
+    // this thread's first.
+    __device__ __forceinline__ void load(const unsigned char *stage, int i, int off, float (&f)[VL]) const
     {
-        if constexpr (VL == 1) {
-            const uint32_t o = skew + at + off + i;
-            f[0] = s != (int)last || (o + 1) * Store<T>::kBytes <= n_last ? load1_rw<T>(stage, o) : load1_rw<T>(p, i);
-        } else {
+        if constexpr (VL == 1)
+            f[0] = load1_rw<T>(stage, skew + at + off + i);
+        else
             Store<T>::unpack(*reinterpret_cast<const uint4 *>(stage + (at + off + i * VL) * Store<T>::kBytes), f);
-        }
     }
 };
 
@@ -416,7 +412,7 @@ struct FwdRing {
     static constexpr int kFit = (int)((kKeep ? 72u : 108u) * 1024 / bytes);
     static constexpr int stages = kFit < 8 ? kFit : 8;
     static constexpr size_t smem = (size_t)stages * bytes;
-    static_assert(stages >= 1, "a row");
+    static_assert(stages >= (VL == 1 ? 2 : 1), "single elements: a barrier between filling a stage and using it");
 };
 
 template <typename T, typename TP, bool RMS, int VL, int NV>
@@ -446,15 +442,13 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
     pdl_wait();
     auto fill = [&](int s, int st) {
         const int64_t a = r0 + (int64_t)s * S, b = a + S < r1 ? a + S : r1;
-        int64_t first;
-        uint32_t n;
-        V::span(a * C, b * C, rows * C, first, n);
-        const uint32_t bar = smem_addr(full + st);
+        const uint32_t bar = smem_addr(full + st), n = V::bytes(a * C, b * C, rows * C);
         mbar_arrive_expect_tx(bar, n);
-        if (n) bulk_load(smem_addr(ring) + st * kBytes, static_cast<const unsigned char *>(x) + first * eb, n, bar);
+        V::copy(ring + st * kBytes, x, a * C, b * C, n, bar);
     };
     if (tid == 0)
         for (int s = 0; s < kRing && s < steps; ++s) fill(s, s);
+    if constexpr (VL == 1) __syncthreads();
 
     float wk[F::kKeep ? NV : 1][VL], bk[F::kKeep ? NV : 1][VL];
     int mine = 0;                                  // this thread's elements of a row
@@ -477,14 +471,13 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
         nl = lane < wpg ? red[0][0][w0 + lane] : 0.f;
         __syncthreads();
     }
-    V view(r0, r1, rows, C, S, slot, g, steps);
+    V view(r0, C, S, slot, g);
     int64_t row = r0 + slot;
     const int64_t at0 = (row * C + g * VL) * eb, hop = S * C * eb;
-    const unsigned char *xp = static_cast<const unsigned char *>(x) + at0;
     unsigned char *yp = static_cast<unsigned char *>(y) + at0;
     int st = 0;
     uint32_t turn = 0;
-    for (int s = 0; s < steps; ++s, row += S, xp += hop, yp += hop) {
+    for (int s = 0; s < steps; ++s, row += S, yp += hop) {
         if (!mbar_wait(smem_addr(full + st), turn)) atomicExch(&g_norm_error, 1u);
         const bool live = row < r1;
         float h[NV][VL];
@@ -493,7 +486,7 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 if (g + j * G < items) {
-                    view.load(ring + st * kBytes, s, xp, j * G, 0, h[j]);
+                    view.load(ring + st * kBytes, j * G, 0, h[j]);
                     if (RMS)
                         v_dot(h[j], h[j], t);
                     else
@@ -862,18 +855,15 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
     pdl_wait();
     auto fill = [&](int s, int st) {
         const int64_t a = r0 + (int64_t)s * SR, b = a + SR < r1 ? a + SR : r1;
-        int64_t first;
-        uint32_t n;
-        V::span(a * C, b * C, rows * C, first, n);
-        const uint32_t bar = smem_addr(full + st), dst = smem_addr(ring) + st * 2 * kBytes;
+        const uint32_t bar = smem_addr(full + st), n = V::bytes(a * C, b * C, rows * C);
+        unsigned char *dst = ring + st * 2 * kBytes;
         mbar_arrive_expect_tx(bar, 2 * n);
-        if (n) {
-            bulk_load(dst, static_cast<const unsigned char *>(x) + first * eb, n, bar);
-            bulk_load(dst + kBytes, static_cast<const unsigned char *>(dy) + first * eb, n, bar);
-        }
+        V::copy(dst, x, a * C, b * C, n, bar);
+        V::copy(dst + kBytes, dy, a * C, b * C, n, bar);
     };
     if (tid == 0)
         for (int s = 0; s < kRing && s < steps; ++s) fill(s, s);
+    if constexpr (VL == 1) __syncthreads();
 
     float wk[F::kKeep ? NV : 1][VL], ag[NV][VL], ab[NV][VL];
 #pragma unroll
@@ -892,12 +882,10 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
             v_mul(d, w, p);
         }
     };
-    V view(r0, r1, rows, C, SR, slot, g, steps);
+    V view(r0, C, SR, slot, g);
     const int row_hop = (int)(S * C);              // elements between a thread's rows of one stage
     int64_t row = r0 + slot;
     const int64_t at0 = (row * C + g * VL) * eb, hop = (int64_t)SR * C * eb, rh = (int64_t)row_hop * eb;
-    const unsigned char *xp = static_cast<const unsigned char *>(x) + at0;
-    const unsigned char *dp = static_cast<const unsigned char *>(dy) + at0;
     unsigned char *op = static_cast<unsigned char *>(dx) + at0;
     float mean_n[R], is_n[R];                      // statistics of the next stage's rows
     auto stats = [&](int64_t from) {
@@ -911,7 +899,7 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
     stats(row);
     int st = 0;
     uint32_t turn = 0;
-    for (int s = 0; s < steps; ++s, row += SR, xp += hop, dp += hop, op += hop) {
+    for (int s = 0; s < steps; ++s, row += SR, op += hop) {
         float mean[R], is[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -931,8 +919,8 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
                 for (int j = 0; j < NV; ++j)
                     if (g + j * G < items) {
                         float h[VL], d[VL], p[VL];
-                        view.load(sx, s, xp + r * rh, j * G, r * row_hop, h);
-                        view.load(sd, s, dp + r * rh, j * G, r * row_hop, d);
+                        view.load(sx, j * G, r * row_hop, h);
+                        view.load(sd, j * G, r * row_hop, d);
                         if (!RMS) v_shift(h, mean[r]);
                         weigh(j, d, p);
                         if (!RMS) v_sum(p, t1);
@@ -954,8 +942,8 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
             for (int j = 0; j < NV; ++j)
                 if (g + j * G < items) {
                     float h[VL], d[VL], p[VL];
-                    view.load(sx, s, xp + r * rh, j * G, r * row_hop, h);
-                    view.load(sd, s, dp + r * rh, j * G, r * row_hop, d);
+                    view.load(sx, j * G, r * row_hop, h);
+                    view.load(sd, j * G, r * row_hop, d);
                     v_center(h, mean[r], is[r]);
                     v_fma(d, h, ag[j]);
                     v_add(d, ab[j]);
@@ -1205,7 +1193,9 @@ cudaError_t fwd_vl(const NormLaunch &a)
     if constexpr (VL > 1)
         if (fwd_warp<T, TP, RMS>(a, &re)) return re;
     if (fwd_ring<T, TP, RMS, VL>(a, &re)) return re;
-    const Group g = pick_group(a.C / VL, a.rows, 16);
+    // 16 vectors a thread in blocks of 256, 8 in blocks of 1024 (64 registers each)
+    Group g = pick_group(a.C / VL, a.rows, 16);
+    if (VL > 1 && g.nv > 8 && (1 << g.lg) > kNormThreads) g = pick_group(a.C / VL, a.rows, 8);
     if (g.nv == 0)
         return launch_pdl(norm_fwd_long_kernel<T, TP, RMS>, dim3((unsigned)a.rows), dim3(kNormMaxThreads), 0, a.stream,
                           a.x, a.gamma, a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C);
@@ -1258,6 +1248,7 @@ bool bwd_ring(const NormLaunch &a, cudaError_t *e)
 template <typename T, typename TP, bool RMS, int VL>
 cudaError_t bwd_vl(const NormLaunch &a)
 {
+    constexpr int kMost = VL == 1 ? 16 : 4;        // items per thread of two tensors, in 64 registers
     cudaError_t fe;
     if (bwd_ring<T, TP, RMS, VL>(a, &fe)) return fe;
     if (a.dgamma || a.dbeta) {
@@ -1272,14 +1263,14 @@ cudaError_t bwd_vl(const NormLaunch &a)
                        a.stream, partial, a.dgamma, a.dbeta, a.C, slabs);
         if (e != cudaSuccess) return e;
     }
-    const Group g = pick_group(a.C / VL, a.rows, 8);
+    const Group g = pick_group(a.C / VL, a.rows, kMost);
     if (g.nv == 0)
         return launch_pdl(norm_dx_long_kernel<T, TP, RMS>, dim3((unsigned)a.rows), dim3(kNormMaxThreads), 0, a.stream,
                           a.x, a.dy, a.gamma, a.mean_in, a.invstd_in, a.out, a.rows, a.C);
     const int threads = (1 << g.lg) > kNormThreads ? (1 << g.lg) : kNormThreads;
     const int64_t per = threads >> g.lg;
     return by_nv(g.nv, [&](auto nv) -> cudaError_t {
-        if constexpr (decltype(nv)::value > 8)
+        if constexpr (decltype(nv)::value > kMost)
             return cudaErrorInvalidValue;
         else
             return launch_pdl(norm_dx_kernel<T, TP, RMS, VL, decltype(nv)::value>,
