@@ -8,7 +8,10 @@
  * and mea_last_error, no allocation, no synchronisation, dense contiguous
  * tensors (unaligned ones take a scalar path unless an entry says otherwise),
  * an element count of zero is a no-op, results bitwise deterministic.
- * bf16 results are rounded once, to nearest even, from fp32 arithmetic.
+ * bf16 results are rounded once, to nearest even, from fp32 arithmetic.  A
+ * bounded wait on a shared-memory barrier that expires in one of these kernels
+ * (which does not happen in correct operation) is recorded in the word that
+ * mea_matmul_error_word reads.
  *
  * Entry points: mea_norm_fwd, mea_norm_bwd (+ _workspace_bytes);
  * mea_matmul_gated_act_fwd, mea_matmul_gated_act_bwd; mea_matmul.
@@ -88,8 +91,8 @@ MEA_API mea_status_t mea_norm_bwd(mea_norm_t norm, mea_dtype_t dtype, mea_dtype_
  *                SwiGLU, MEA_GELU_*: GeGLU, MEA_RELU: ReGLU, MEA_SIGMOID: GLU).
  *   M, N, K      X is [M x K], Wg and Wu are [N x K], h is [M x N]; M or N of
  *                0 is a no-op; K must be positive.  K and N must be multiples
- *                of 8, each below 2^31; otherwise MEA_ERR_UNSUPPORTED.  Any M
- *                from one token up.
+ *                of 8, M, N and K below 2^31 - 1024; otherwise
+ *                MEA_ERR_UNSUPPORTED.  Any M from one token up.
  *   x, w_gate,
  *   w_up         device, bf16, row-major (K contiguous), read only, 16-byte
  *                aligned (else MEA_ERR_UNSUPPORTED).  The two weights may be
@@ -135,8 +138,8 @@ MEA_API mea_status_t mea_matmul_gated_act_bwd(mea_act_t act, int64_t M, int64_t 
  *   trans_a      zero: A is [M x K]; non-zero: A is [K x M] and op(A) = A^T.
  *   trans_b      zero: B is [K x N]; non-zero: B is [N x K] and op(B) = B^T.
  *                Both non-zero is MEA_ERR_UNSUPPORTED.
- *   M, N, K      each below 2^31; M or N of 0 is a no-op, K of 0 sets C to
- *                zero.  The rows of A, B and C as stored must be multiples of
+ *   M, N, K      each below 2^31 - 1024; M or N of 0 is a no-op, K of 0 sets C
+ *                to zero.  The rows of A, B and C as stored must be multiples of
  *                8 elements (else MEA_ERR_UNSUPPORTED).
  *   a, b         device, bf16, row-major, read only, 16-byte aligned.
  *   c            device, bf16, [M x N], written, 16-byte aligned; overlaps

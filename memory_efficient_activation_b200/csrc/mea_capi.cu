@@ -714,10 +714,20 @@ mea_status_t mea_matmul_act_bwd(mea_act_t act, int64_t M, int64_t N, int64_t K, 
     return e == cudaSuccess ? MEA_OK : cuda_fail(e, "mea_matmul_act_bwd launch");
 }
 
+// Row and column numbers of a tile that reaches over the edge stay in 32 bits.
+static mea_status_t check_block_sizes(int act, int64_t M, int64_t N, int64_t K)
+{
+    mea_status_t st = check_matmul("", act, M, N, K);
+    if (st != MEA_OK) return st;
+    const int64_t lim = ((int64_t)1 << 31) - 1024;
+    if (M >= lim || N >= lim || K >= lim) return fail(MEA_ERR_UNSUPPORTED, "M, N and K must be below 2^31 - 1024");
+    return MEA_OK;
+}
+
 // M, N and K of a gated product; *done is set where there is nothing to do.
 static mea_status_t check_gated(int act, int64_t M, int64_t N, int64_t K, bool *done)
 {
-    mea_status_t st = check_matmul("", act, M, N, K);
+    mea_status_t st = check_block_sizes(act, M, N, K);
     *done = st == MEA_OK && (M == 0 || N == 0);
     if (st != MEA_OK || *done) return st;
     if (K == 0) return fail(MEA_ERR_UNSUPPORTED, "K = 0 (an empty product) is not served");
@@ -805,7 +815,7 @@ mea_status_t mea_matmul(int trans_a, int trans_b, int64_t M, int64_t N, int64_t 
 {
     Range range_("mea_matmul");
     clear_error();
-    mea_status_t st = check_matmul("", MEA_RELU, M, N, K);
+    mea_status_t st = check_block_sizes(MEA_RELU, M, N, K);
     if (st != MEA_OK) return st;
     if (trans_a && trans_b) return fail(MEA_ERR_UNSUPPORTED, "both operands transposed is not served");
     if (M == 0 || N == 0) return MEA_OK;

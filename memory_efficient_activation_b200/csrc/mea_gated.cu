@@ -23,7 +23,7 @@
 //   backward   each CTA stages 128 columns of Wd as it is stored ([K x N], N
 //              contiguous): the operand is read N-major, no transposed copy
 //              of the weight is made.
-// Output tiles go round-robin to CTA pairs in groups of kGroupM row tiles
+// Output tiles go round-robin to CTA pairs in groups of 8 or 16 row tiles
 // with the rows fastest, so that the pairs at work at one time share a few
 // tiles of both operands in L2 (by columns alone, 64 column tiles of a 134 MB
 // weight would stream from HBM once per row tile).  Every tile's sum runs
@@ -57,7 +57,6 @@ constexpr int kAcc = 256;                                   // accumulator colum
 constexpr int kBK = 64;                                     // K per pipeline stage: 128 bytes
 constexpr int kHalf = 128;                                  // rows (columns) of A and B one CTA stages
 constexpr int kUmmaK = 16;
-constexpr int kGroupM = 8;                                  // row tiles per group of the tile order
 constexpr uint32_t kStageA = kHalf * kBK * 2;               // 16 KB
 constexpr uint32_t kStageBytes = 2 * kStageA;
 constexpr uint32_t kTmemCols = 2 * kAcc;                    // 512: all of tensor memory
@@ -71,6 +70,10 @@ struct Shape {
     static constexpr bool kMMajorA = MODE == kPlainTN;
     static constexpr bool kNMajorB = MODE == kBwd || MODE == kPlainNN || MODE == kPlainTN;
     static constexpr int kTN = MODE == kFwd ? kHalf : kAcc;              // output columns of a tile
+    // Row tiles per group of the tile order, measured back to back under the
+    // power limit: 16 for the forward ([8192 x 2 x 8192 x 4096] 831 us against
+    // 844 at 8 and 883 at 4), 8 elsewhere (backward 498; 508 at 16, 523 at 4).
+    static constexpr int kGroupM = MODE == kFwd ? 16 : 8;
     // Epilogue warps: one per quarter of tensor memory.  Eight for the backward
     // (each half of the columns) hide more latency but take 40 KB more of
     // chunk buffers, one pipeline stage: slower (at [4096 x 10928 x 2048] 220
@@ -80,14 +83,14 @@ struct Shape {
     // Chunk buffers per warp.  Backward: gate and up as they arrive, of two
     // chunks (read into registers at once, so that two more are on their way
     // during the arithmetic: 32 KB in flight per SM), dgate, dup and h.
-    // Forward: gate, up and h, plain: C, kOut sets of them in turn: a store
-    // reads its chunk some 1000 cycles after it was issued, which one set
-    // would wait for every time.
-    static constexpr int kOut = MODE == kBwd ? 1 : MODE == kFwd ? 2 : 4;
-    static constexpr int kChunks = MODE == kBwd ? 7 : MODE == kFwd ? 3 * kOut : kOut;
+    // Forward: gate, up and h; a second set of them would cost a pipeline
+    // stage (157 against 163 us at [4096 x 2 x 5464 x 2048]).  Plain: four of
+    // C in turn.
+    static constexpr int kOut = MODE == kBwd || MODE == kFwd ? 1 : 4;
+    static constexpr int kChunks = MODE == kBwd ? 7 : MODE == kFwd ? 3 : kOut;
     static constexpr uint32_t kEpiBytes = kWarps * kChunks * kChunk;
     // Pipeline stages: what is left of the shared memory.
-    static constexpr int kStages = MODE == kBwd || MODE == kFwd ? 5 : 6;
+    static constexpr int kStages = MODE == kBwd ? 5 : 6;
     static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiBytes + 256;
     static_assert(kSmemBytes <= 232448, "shared memory of a block");
 };
@@ -110,14 +113,15 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr)
 
 __device__ __forceinline__ void record_error() { atomicExch(&g_gated_error, 1u); }
 
-// Row and column tile of the t-th tile: groups of kGroupM row tiles, rows
-// fastest within a group.
+// Row and column tile of the t-th tile: groups of GM row tiles, rows fastest
+// within a group.
+template <int GM>
 __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int &tm, int &tn)
 {
-    const int per = kGroupM * tiles_n, g = t / per, r = t - g * per;
-    const int left = tiles_m - g * kGroupM, rows = left < kGroupM ? left : kGroupM;
+    const int per = GM * tiles_n, g = t / per, r = t - g * per;
+    const int left = tiles_m - g * GM, rows = left < GM ? left : GM;
     tn = r / rows;
-    tm = g * kGroupM + r - tn * rows;
+    tm = g * GM + r - tn * rows;
 }
 
 // Row `lane` of a chunk in shared memory, 32 bf16 as 16 words.  The 64-byte
@@ -420,7 +424,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
                 int tm, tn;
-                tile_of(t, tiles_m, tiles_n, tm, tn);
+                tile_of<S::kGroupM>(t, tiles_m, tiles_n, tm, tn);
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const int s = it % kStages, round = it / kStages;
                     if (round > 0 && !mbar_wait(smem_addr(empty + s), (round & 1) ^ 1)) {
@@ -514,7 +518,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
         };
         auto place = [&](int t) {
             int tm, tn;
-            tile_of(t, tiles_m, tiles_n, tm, tn);
+            tile_of<S::kGroupM>(t, tiles_m, tiles_n, tm, tn);
             Place p;
             p.row = tm * kBM + row_in;
             p.col = tn * kTN + c0 * 32;
@@ -570,7 +574,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                 uint32_t v[32], w[16];
                 tmem_ld32(lanes + (c0 + c) * 32, v);
                 const int row = p.row, col = p.col + c * 32;
-                const uint32_t buf = mine + (MODE == kBwd ? 4 : n % S::kOut * (MODE == kFwd ? 3 : 1)) * kChunk;
+                const uint32_t buf = mine + (MODE == kBwd ? 4 : n % S::kOut) * kChunk;
                 if constexpr (MODE == kFwd) {
                     uint32_t u[32];
                     tmem_ld32(lanes + kHalf + (c0 + c) * 32, u);
@@ -722,7 +726,7 @@ cudaError_t gated_error_word(int clear, unsigned int *word)
 // 32.9 / 36.9; 128 tiles, M 64 63.5 / 69.6 and 128 72.7 / 69.6).
 bool few_tokens(int64_t M, int64_t tiles)
 {
-    const int64_t pairs = sm_count() / 2;
+    constexpr int64_t pairs = kB200Sms / 2;
     return M <= 64 || (M <= 128 && tiles <= pairs) || (M <= kFewTokens && 2 * tiles <= pairs);
 }
 

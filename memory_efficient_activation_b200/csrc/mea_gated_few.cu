@@ -312,7 +312,7 @@ cudaError_t launch_few_one(const GatedLaunch &g)
     const uint32_t stage = kBytesW + (uint32_t)a.mt * (kBK * 2);
     const int per_sm = stage <= 24 * 1024 ? 2 : 1;
     int ks = 1;
-    while (ks < 8 && tiles * ks * 2 <= (int64_t)sm_count() * per_sm && kb >= ks * 2 * 4) ks *= 2;
+    while (ks < 8 && tiles * ks * 2 <= (int64_t)kB200Sms * per_sm && kb >= ks * 2 * 4) ks *= 2;
     const uint32_t budget = (uint32_t)kFewSmemMax / per_sm - 2048;
     a.stages = (int)(budget / stage) < 8 ? (int)(budget / stage) : 8;
     a.tmem_cols = 32;

@@ -101,6 +101,10 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// SMs of a B200.  Rules that choose between kernels or split a sum use this
+// number, not the device's, so that results do not depend on it.
+constexpr int kB200Sms = 148;
+
 // Resident blocks per SM of one kernel instantiation at `threads` threads
 // per block.  The Tag type gives every instantiation its own cache (kernels
 // of one template share a function-pointer type).  Every GPU this library

@@ -34,7 +34,7 @@ namespace {
 constexpr int kNormThreads = 256;      // threads of a block (more where one row needs more)
 constexpr int kNormMaxThreads = 1024;
 constexpr int kSlabRows = 1024;        // most rows whose terms one fp32 column sum takes
-constexpr int kSlabs = 148;            // column-sum slabs of a large tensor (one per SM of a B200)
+constexpr int kSlabs = kB200Sms;       // column-sum slabs of a large tensor
 constexpr int64_t kRingBytes = 4 << 20;   // the forward streams through a ring from this size of x on
 constexpr int kColX = 32, kColY = 8;   // threads of a column-sum block: columns x rows
 
@@ -1091,7 +1091,7 @@ struct Group {
 inline Group pick_group(int64_t items, int64_t rows, int nv_max)
 {
     int nv_want = nv_max;
-    while (nv_want > 1 && rows * ((items + nv_want - 1) / nv_want) < (int64_t)148 * 1024) nv_want >>= 1;
+    while (nv_want > 1 && rows * ((items + nv_want - 1) / nv_want) < (int64_t)kB200Sms * 1024) nv_want >>= 1;
     int lg = 5;
     while (lg < 10 && ((int64_t)nv_want << lg) < items) ++lg;
     int nv = 1;
@@ -1169,7 +1169,7 @@ template <typename T, typename TP, bool RMS>
 bool fwd_warp(const NormLaunch &a, cudaError_t *e)
 {
     const int64_t items = a.C / Store<T>::V, grid = 2 * sm_count();
-    if (items <= 32 || items > 512 || a.rows < grid * (kWarpThreads / 32)) return false;
+    if (items <= 32 || items > 512 || a.rows < 2 * kB200Sms * (kWarpThreads / 32)) return false;
     constexpr int kParam = Store<T>::V * Store<TP>::kBytes * 2 < 16 ? 16 : Store<T>::V * Store<TP>::kBytes * 2;
     int nv = 2;
     while (nv * 32 < items) nv <<= 1;

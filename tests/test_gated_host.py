@@ -52,6 +52,7 @@ def test_gated_fwd_validation(lib):
 
     assert fwd(act=7) == INV and fwd(M=-1) == INV and fwd(N=-8) == INV and fwd(K=-8) == INV
     assert fwd(M=1 << 31) == UNS and fwd(N=1 << 31) == UNS and fwd(K=0) == UNS
+    assert fwd(M=(1 << 31) - 1024) == UNS                      # a tile's last row number would pass 31 bits
     assert fwd(K=12) == UNS and fwd(N=12) == UNS
     assert fwd(x=None) == INV and fwd(wg=None) == INV and fwd(wu=None) == INV and fwd(z=None, h=None) == INV
     assert fwd(x=P + 8) == UNS and fwd(wg=2 * P + 2) == UNS and fwd(wu=3 * P + 4) == UNS
