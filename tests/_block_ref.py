@@ -113,7 +113,7 @@ def act(name, z, param=1.0):
         s, c = torch.special.expit(u2), torch.special.expit(-u2)
         return z * s, s + z * s * c * 2 * k * (1 + 3 * 0.044715 * z * z)
     assert name == "gelu_erf", name
-    p = torch.special.ndtr(z)
+    p = 0.5 * torch.erfc(-z / math.sqrt(2))      # not 1 + erf, which is zero below -8.3
     return z * p, p + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
 
 

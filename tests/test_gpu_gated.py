@@ -94,6 +94,30 @@ def test_gated_many_tiles(M, N, K):
     _bwd("swish", M, N, K, M + N + 1)
 
 
+@pytest.mark.parametrize("M,N,K", [(64, 9608, 72), (65, 9608, 72), (100, 9408, 72), (129, 4808, 72), (200, 4664, 72)])
+def test_gated_either_side_of_the_kernels_border(M, N, K):
+    """Few tokens with many and with few column tiles: both kernels."""
+    _fwd("gelu_erf", M, N, K, M + N)
+
+
+@pytest.mark.parametrize("act,param", [(a, _p(a)) for a in ACTS] + [("swish", 1.0), ("swish", -0.7), ("swish", 0.0)])
+def test_gated_bwd_extreme_gates(act, param):
+    """Gates far out on both sides, and a dense band around the zeros of f'."""
+    g = _gen(16)
+    M, N, K = 40, 264, 72
+    dout, wd = _normal(g, M, K), _normal(g, K, N, scale=K ** -0.5)
+    gate = torch.empty(M, N, device="cuda")
+    gate[:20] = torch.linspace(-1.6, -0.6, 20 * N, device="cuda").view(20, N)
+    far = torch.tensor([0.0, 5.0, 12.0, 13.5, 20.0, 60.0, 88.0, 100.0, 1e3, 1e6, 1e15, 1e30], device="cuda")
+    gate[20:] = torch.cat([far, -far]).repeat(20 * N // 24)[:20 * N].view(20, N)
+    z = torch.cat([gate, torch.ones(M, N, device="cuda")], 1).to(BF)
+    dz, h = mea.matmul_gated_act_bwd(act, dout, wd, z, param)
+    rdz, rh = ref.gated_bwd(act, dout, wd, z, param)
+    bdz, bh = ref.gated_bwd_bounds(act, dout, wd, z, param)
+    ref.assert_within(dz, rdz, bdz, "dz")
+    ref.assert_within(h, rh, bh, "h")
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_gated_outputs_skipped(M):
     a = _fwd("gelu_tanh", M, 264, 136, 5)

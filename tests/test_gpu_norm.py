@@ -60,6 +60,16 @@ def test_norm_many_rows(norm, dtype, rows, C):
     _check(norm, x, dy, gamma, beta)
 
 
+@pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("dtype,pdtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,C", [(2400, 264), (2369, 512), (2401, 2048), (300, 16384), (4099, 1001), (2100, 1003)])
+def test_norm_streamed_rows(norm, dtype, pdtype, rows, C):
+    """Rows enough for the streaming kernels (a warp to a row; rings of every
+    width; single elements), each with both parameter types."""
+    x, dy, gamma, beta = _inputs(rows, C, dtype, pdtype, rows * 3 + C)
+    _check(norm, x, dy, gamma, beta)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,C", [(2, 131072), (2, 131073), (1, 300001)])
 def test_norm_rows_longer_than_a_block_holds(dtype, rows, C):
@@ -106,6 +116,31 @@ def test_norm_bad_values_stay_in_their_row(norm):
     assert torch.equal(y[keep], clean[0][keep]) and y[2].isnan().all()
     dx = mea.norm_bwd(norm, x, dy, gamma, mean, invstd)[0]
     assert torch.equal(dx[keep], dxc[keep]) and dx[2].isnan().all()
+
+
+@pytest.fixture(autouse=True)
+def no_expired_waits():
+    yield
+    from memory_efficient_activation_b200 import _capi
+    assert _capi.lib().mea_matmul_error_word(1) == 0
+
+
+def test_norm_two_calls_at_once():
+    """The same tensors normalised on two streams at the same time: the
+    workspaces are per call."""
+    x, dy, gamma, beta = _inputs(6000, 1024, "bf16", "bf16", 14)
+    y, mean, invstd = mea.norm_fwd("layer", x, gamma, beta)
+    want = mea.norm_bwd("layer", x, dy, gamma, mean, invstd, want_dbeta=True)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append((mea.norm_fwd("layer", x, gamma, beta)[0],
+                            mea.norm_bwd("layer", x, dy, gamma, mean, invstd, want_dbeta=True)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, y) and all(torch.equal(p, q) for p, q in zip(b, want))
 
 
 def test_norm_no_rows():
