@@ -65,7 +65,11 @@ constexpr uint32_t kTmemCols = 2 * kAcc;                    // 512: all of tenso
 // row in shared memory under the 64-byte swizzle, moved by TMA.
 constexpr uint32_t kChunk = 32 * 32 * 2;
 
-template <Mode MODE>
+// EW: epilogue warps, four (one per quarter of tensor memory) or eight (each
+// half of the columns too).  Four, with more pipeline stages, where a pair of
+// SMs has several tiles and the epilogue of one runs beside the matmul of the
+// next; eight where it has one and nothing hides the epilogue.
+template <Mode MODE, int EW>
 struct Shape {
     static constexpr bool kMMajorA = MODE == kPlainTN;
     static constexpr bool kNMajorB = MODE == kBwd || MODE == kPlainNN || MODE == kPlainTN;
@@ -74,23 +78,20 @@ struct Shape {
     // power limit: 16 for the forward ([8192 x 2 x 8192 x 4096] 831 us against
     // 844 at 8 and 883 at 4), 8 elsewhere (backward 498; 508 at 16, 523 at 4).
     static constexpr int kGroupM = MODE == kFwd ? 16 : 8;
-    // Epilogue warps: one per quarter of tensor memory.  Eight for the backward
-    // (each half of the columns) hide more latency but take 40 KB more of
-    // chunk buffers, one pipeline stage: slower (at [4096 x 10928 x 2048] 220
-    // us against 196).
-    static constexpr int kWarps = 4;
+    static constexpr int kWarps = EW;
     static constexpr int kThreads = 64 + 32 * kWarps;
-    // Chunk buffers per warp.  Backward: gate and up as they arrive, of two
-    // chunks (read into registers at once, so that two more are on their way
-    // during the arithmetic: 32 KB in flight per SM), dgate, dup and h.
-    // Forward: gate, up and h; a second set of them would cost a pipeline
-    // stage (157 against 163 us at [4096 x 2 x 5464 x 2048]).  Plain: four of
-    // C in turn.
+    // Chunk buffers per warp.  Backward: gate and up as they arrive (read into
+    // registers at once, so that the next are on their way during the
+    // arithmetic; of two chunks with four warps, 32 KB in flight per SM),
+    // dgate, dup and h.  Forward: gate, up and h; a second set of them would
+    // cost a pipeline stage (157 against 163 us at [4096 x 2 x 5464 x 2048]).
+    // Plain: C in turn.
+    static constexpr int kIn = MODE == kBwd ? 8 / EW : 0;
     static constexpr int kOut = MODE == kBwd || MODE == kFwd ? 1 : 4;
-    static constexpr int kChunks = MODE == kBwd ? 7 : MODE == kFwd ? 3 : kOut;
+    static constexpr int kChunks = MODE == kBwd ? 2 * kIn + 3 : MODE == kFwd ? 3 : kOut;
     static constexpr uint32_t kEpiBytes = kWarps * kChunks * kChunk;
     // Pipeline stages: what is left of the shared memory.
-    static constexpr int kStages = MODE == kBwd ? 5 : 6;
+    static constexpr int kStages = MODE == kBwd ? (EW == 8 ? 4 : 5) : 6;
     static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiBytes + 256;
     static_assert(kSmemBytes <= 232448, "shared memory of a block");
 };
@@ -99,17 +100,6 @@ struct Shape {
 // M 256; A K-major or M-major (bit 15), B K-major or N-major (bit 16).
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kAcc >> 3) << 17) |
                             ((uint32_t)(kBM >> 4) << 24);
-
-// Shared-memory descriptor of an M- or N-major operand tile written by TMA
-// with the 128-byte swizzle: each k row holds 64 contiguous elements of M or N
-// (128 bytes), 8-row groups of k lie 1024 bytes apart (stride byte offset),
-// and the next 64 elements lie 64 x 128 = 8192 bytes on (leading byte
-// offset).  A K step of 16 advances the start address by 16 rows, 2048 bytes.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr)
-{
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
 
 __device__ __forceinline__ void record_error() { atomicExch(&g_gated_error, 1u); }
 
@@ -355,11 +345,11 @@ struct Maps {
     CUtensorMap x, w0, w1, in0, in1, out0, out1, out2;
 };
 
-template <class A, Mode MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThreads, 1)
+template <class A, Mode MODE, int EW>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE, EW>::kThreads, 1)
 gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param, int want01, int want2)
 {
-    using S = Shape<MODE>;
+    using S = Shape<MODE, EW>;
     constexpr int kTN = S::kTN, kStages = S::kStages;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -506,6 +496,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
         const Coef k = A::coef(param);
         const uint32_t release = cluster_addr(smem_addr(acc_empty), 0);
         const uint32_t mine = ebase + ew * (S::kChunks * kChunk);
+        constexpr int kIn = S::kIn > 0 ? S::kIn : 1;
         constexpr int kHalves = S::kWarps / 4, kMost = kTN / 32 / kHalves;   // column shares, chunks of one
         const int c0 = (ew >> 2) * kMost;                  // this warp's first chunk
         const uint32_t in_bars = smem_addr(in_full + 2 * ew);
@@ -539,7 +530,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
         auto fetch = [&] {
             if (ft >= ntiles) return;
             if (lane == 0) {
-                const uint32_t dst = mine + (fetched & 1) * 2 * kChunk, bar = in_bars + 8 * (fetched & 1);
+                const uint32_t k = fetched % kIn, dst = mine + k * 2 * kChunk, bar = in_bars + 8 * k;
                 mbar_arrive_expect_tx(bar, 2 * kChunk);
                 chunk_load(dst, &maps.in0, fp.col + fc * 32, fp.row, bar);
                 chunk_load(dst + kChunk, &maps.in1, fp.col + fc * 32, fp.row, bar);
@@ -555,8 +546,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
         bool ok = true;
         if constexpr (MODE == kBwd) {
             seek();
-            fetch();
-            fetch();
+            for (int i = 0; i < kIn; ++i) fetch();
         }
         int lt = 0;
         for (int t = pair; t < ntiles; t += npairs, ++lt) {
@@ -574,7 +564,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                 uint32_t v[32], w[16];
                 tmem_ld32(lanes + (c0 + c) * 32, v);
                 const int row = p.row, col = p.col + c * 32;
-                const uint32_t buf = mine + (MODE == kBwd ? 4 : n % S::kOut) * kChunk;
+                const uint32_t buf = mine + (MODE == kBwd ? 2 * kIn : n % S::kOut) * kChunk;
                 if constexpr (MODE == kFwd) {
                     uint32_t u[32];
                     tmem_ld32(lanes + kHalf + (c0 + c) * 32, u);
@@ -592,8 +582,8 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                     }
                 } else if constexpr (MODE == kBwd) {
                     uint32_t uw[16], hw[16];
-                    const uint32_t in = mine + (n & 1) * 2 * kChunk;
-                    if (!mbar_wait(in_bars + 8 * (n & 1), (n >> 1) & 1)) {
+                    const uint32_t in = mine + n % kIn * 2 * kChunk;
+                    if (!mbar_wait(in_bars + 8 * (n % kIn), (n / kIn) & 1)) {
                         record_error();
                         ok = false;
                         break;
@@ -632,7 +622,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
         }
         // what is in flight has landed before this CTA's memory goes away
         for (; n < fetched; ++n)
-            if (!mbar_wait(in_bars + 8 * (n & 1), (n >> 1) & 1)) record_error();
+            if (!mbar_wait(in_bars + 8 * (n % kIn), (n / kIn) & 1)) record_error();
         if (lane == 0) store_wait_read<0>();
     }
     pdl_trigger();
@@ -653,10 +643,21 @@ bool chunk_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, i
     return bf16_map(map, base, rows, cols, ld, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+template <class A, Mode MODE, int EW>
+cudaError_t launch_warps(const GatedLaunch &a, const Maps &m, int pairs)
+{
+    using S = Shape<MODE, EW>;
+    auto kernel = gated_kernel<A, MODE, EW>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(S::kThreads), S::kSmemBytes, a.stream, m, (int)a.M,
+                      (int)a.N, (int)a.K, a.param, (int)(a.z != nullptr), (int)(a.h != nullptr));
+}
+
 template <class A, Mode MODE>
 cudaError_t launch_one(const GatedLaunch &a)
 {
-    using S = Shape<MODE>;
+    using S = Shape<MODE, 4>;
     Maps m;
     // an operand stored with K contiguous: boxes of 128 rows x 64 k; one with
     // M or N contiguous: boxes of 64 k x 64
@@ -675,14 +676,14 @@ cudaError_t launch_one(const GatedLaunch &a)
         ok = ok && chunk_map(&m.out0, z, a.M, a.N, a.N);
     }
     if (!ok) return cudaErrorInvalidValue;
-    auto kernel = gated_kernel<A, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmemBytes);
-    if (e != cudaSuccess) return e;
     const int64_t tiles = ((a.M + kBM - 1) / kBM) * ((a.N + S::kTN - 1) / S::kTN);
-    const int pairs_max = sm_count() / 2;
-    const int pairs = (int)(tiles < pairs_max ? tiles : pairs_max);
-    return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(S::kThreads), S::kSmemBytes, a.stream, m, (int)a.M,
-                      (int)a.N, (int)a.K, a.param, (int)(z != nullptr), (int)(a.h != nullptr));
+    const int pairs = sm_count() / 2;
+    // The forward and the plain products, whose epilogue does little, gained
+    // nothing from eight warps; the backward 5 to 12 percent ([1023 x 2728 x
+    // 1024] 18.7 -> 17.7 us, [300 x 2048 x 512] 14.9 -> 13.1).
+    if constexpr (MODE == kBwd)
+        if (tiles <= pairs) return launch_warps<A, MODE, 8>(a, m, (int)tiles);
+    return launch_warps<A, MODE, 4>(a, m, (int)(tiles < pairs ? tiles : pairs));
 }
 
 template <Mode MODE>
@@ -718,6 +719,18 @@ cudaError_t gated_error_word(int clear, unsigned int *word)
     return e;
 }
 
+// Whether a product of `tiles` tiles of this kernel has its K shared out
+// instead (launch_few): where more than half of the SM pairs would idle and K
+// is long beside the tiles.  Measured (us, this kernel / shared out; tiles,
+// K blocks): 16, 86 29.0 / 16.8; 16, 43 21.3 / 14.9; 4, 32 13.8 / 8.1; 16, 24
+// 11.6 / 10.5; 32, 64 23.0 / 21.2; 16, 16 9.4 / 9.7; 24, 16 9.5 / 12.2; 32, 32
+// 14.0 / 14.9.
+bool share_k(int64_t tiles, int64_t K)
+{
+    const int64_t kb = (K + kBK - 1) / kBK;
+    return 2 * tiles <= kB200Sms / 2 && kb >= 20 && 2 * kb >= 3 * tiles;
+}
+
 // Whether the few-token kernel serves M rows with `tiles` column tiles of this
 // kernel.  Up to 64 rows always: this kernel would multiply mostly zeros.
 // Beyond, while the tiles leave pairs of SMs idle that shares of K use: all
@@ -732,8 +745,13 @@ bool few_tokens(int64_t M, int64_t tiles)
 
 cudaError_t launch_gated(const GatedLaunch &a)
 {
-    if (a.mode == 1) return by_act<kBwd>(a);
-    return few_tokens(a.M, (a.N + kHalf - 1) / kHalf) ? launch_few(a, true) : by_act<kFwd>(a);
+    const int64_t rows = (a.M + kBM - 1) / kBM;
+    // the backward's heavier epilogue is not hidden there: one tile of tokens
+    // ([100 x 4096 x 2048] 21.6 -> 9.4 us, but [512 x 1024 x 2048] 19.6 -> 21.4)
+    if (a.mode == 1)
+        return a.M <= kFewTokens && share_k((a.N + kAcc - 1) / kAcc, a.K) ? launch_few(a, kFewBwd) : by_act<kBwd>(a);
+    const int64_t cols = (a.N + kHalf - 1) / kHalf;
+    return few_tokens(a.M, cols) || share_k(rows * cols, a.K) ? launch_few(a, kFewGated) : by_act<kFwd>(a);
 }
 
 cudaError_t launch_matmul(const MatmulPlain &p)
@@ -746,10 +764,11 @@ cudaError_t launch_matmul(const MatmulPlain &p)
     a.w0 = p.b;
     a.z = p.c;
     a.stream = p.stream;
+    const int64_t cols = (a.N + kAcc - 1) / kAcc, tiles = (a.M + kBM - 1) / kBM * cols;
+    const FewKind kind = p.trans_a ? kFewTN : p.trans_b ? kFewNT : kFewNN;
+    if ((!p.trans_a && few_tokens(a.M, cols)) || share_k(tiles, a.K)) return launch_few(a, kind);
     if (p.trans_a) return launch_one<ReLU, kPlainTN>(a);
-    if (p.trans_b)
-        return few_tokens(a.M, (a.N + kAcc - 1) / kAcc) ? launch_few(a, false) : launch_one<ReLU, kPlainNT>(a);
-    return launch_one<ReLU, kPlainNN>(a);
+    return p.trans_b ? launch_one<ReLU, kPlainNT>(a) : launch_one<ReLU, kPlainNN>(a);
 }
 
 }  // namespace mea

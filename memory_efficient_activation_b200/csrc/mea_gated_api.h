@@ -41,10 +41,13 @@ struct MatmulPlain {
     cudaStream_t stream;
 };
 
-// Few tokens: the forward's (gated) or a plain product with a [N x K] weight
-// (x = A, w0 = B, z = C), M at most kFewTokens.
+// Products of few output tiles, K shared out over a cluster: the gated
+// forward, its backward, or a plain one (x = A, w0 = B, z = C; NT: B is [N x
+// K], NN: [K x N], TN: A is [K x M] and B [K x N]).  Tiles of kFewTokens rows
+// at most.
 constexpr int kFewTokens = 256;
-cudaError_t launch_few(const GatedLaunch &a, bool gated);
+enum FewKind { kFewGated, kFewBwd, kFewNT, kFewNN, kFewTN };
+cudaError_t launch_few(const GatedLaunch &a, FewKind kind);
 cudaError_t few_error_word(int clear, unsigned int *word);     // synchronous
 cudaError_t launch_matmul(const MatmulPlain &p);
 cudaError_t launch_gated(const GatedLaunch &a);

@@ -25,6 +25,17 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr)
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// Shared-memory descriptor of an M- or N-major operand tile written by TMA
+// with the 128-byte swizzle: each k row holds 64 contiguous elements of M or N
+// (128 bytes), 8-row groups of k lie 1024 bytes apart (stride byte offset),
+// and the next 64 elements lie 64 x 128 = 8192 bytes on (leading byte
+// offset).  A K step of 16 advances the start address by 16 rows, 2048 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
 // TMA load into this CTA's shared memory that completes on `bar`, a
 // shared::cluster address that may lie in the other CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
