@@ -8,12 +8,27 @@
 //              dx = invstd (a - m1 - xhat m2),
 //              dgamma = sum over rows of dy xhat, dbeta = sum over rows of dy
 //
-// Both are bound by memory (8 to 14 operations per element).  A row is held
-// in registers between its reduction and its output, so each tensor is read
-// once: a group of threads owns a row, a power of two from 32 threads (whole
-// reduction by shuffles) to a block.  The variance is a second pass over the
-// registers (sum of (x - mean)^2), not a difference of two large sums.  Row
-// sums are fp32: up to 32 terms in sequence in a thread, then a tree.
+// Both are bound by memory (8 to 14 operations per element), so each tensor is
+// read once.  The variance is a second pass over the row on chip (sum of (x -
+// mean)^2), not a difference of two large sums.  Row sums are fp32, short
+// sequences in a thread and then a tree; column sums take at most 1024 rows in
+// fp32 and add those in fp64.  Every kernel's results are rounded once.
+//
+// Forward, by shape:
+//   many rows of 33 to 512 vectors    a warp to a row, in registers
+//   other large tensors               blocks over shared-memory rings
+//   small tensors (below 4 MB)        a row spread over more threads
+//   rows no block's registers hold    three passes over the row
+// Backward:
+//   rows that 512 threads hold        one pass over x and dy for dx and the
+//                                     column sums, over shared-memory rings
+//   longer rows, unaligned tensors    column sums, then dx
+//
+// Measured, 16384 x 4096 bf16 with fp32 parameters: forward 45 us (5.9 TB/s),
+// backward 81 us (5.0 TB/s) with dgamma and dbeta, 74 without.  What bounds
+// the backward is latency at 16 warps per SM: 181 instructions a warp and 256
+// elements issue in 55 percent of the cycles, two blocks of 64 registers (and
+// two rows between barriers) were slower.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -35,7 +50,10 @@ constexpr int kNormThreads = 256;      // threads of a block (more where one row
 constexpr int kNormMaxThreads = 1024;
 constexpr int kSlabRows = 1024;        // most rows whose terms one fp32 column sum takes
 constexpr int kSlabs = kB200Sms;       // column-sum slabs of a large tensor
-constexpr int64_t kRingBytes = 4 << 20;   // the forward streams through a ring from this size of x on
+// Size of x from which the forward streams through a ring (us, one row per
+// group of threads / ring: 1001 bf16 channels, 2 MB 3.9 / 6.8, 4 MB 8.9 / 8.8,
+// 8 MB 22.0 / 12.0; 144 bf16 2 MB 2.6 / 3.1, 8 MB 8.5 / 8.1).
+constexpr int64_t kRingBytes = 4 << 20;
 constexpr int kColX = 32, kColY = 8;   // threads of a column-sum block: columns x rows
 
 // Column-sum slabs, from the row count and the rows a block takes at a time
