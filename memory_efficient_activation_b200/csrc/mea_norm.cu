@@ -915,6 +915,7 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
         }
     };
     stats(row);
+    int left = row < r1 ? (int)((r1 - row + S - 1) / S) : 0;   // rows of this slot still to come
     int st = 0;
     uint32_t turn = 0;
     for (int s = 0; s < steps; ++s, row += SR, op += hop) {
@@ -927,7 +928,8 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
         if (!mbar_wait(smem_addr(full + st), turn)) atomicExch(&g_norm_error, 1u);
         stats(row + SR);
         const unsigned char *sx = ring + st * 2 * kBytes, *sd = sx + kBytes;
-        const int live = row < r1 ? (int)((r1 - row + S - 1) / S < R ? (r1 - row + S - 1) / S : R) : 0;   // this slot's rows
+        const int live = left < R ? left : R;      // this slot's rows in the stage
+        left = left < R ? 0 : left - R;
         float v[N];
 #pragma unroll
         for (int r = 0; r < R; ++r) {

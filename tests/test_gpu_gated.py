@@ -337,3 +337,13 @@ def test_matmul_empty_and_guarded():
     mea.matmul(torch.ones(37, 16, dtype=BF, device="cuda"), torch.ones(16, 40, dtype=BF, device="cuda"),
                out=buf[64:64 + 37 * 40].view(37, 40))
     assert (buf[:64] == 7).all() and (buf[-64:] == 7).all() and (buf[64:-64] == 16).all()
+
+
+@pytest.mark.parametrize("norm", [None, "layer"])
+def test_gated_block_of_no_tokens(norm):
+    m = mea.MemoryEfficientGatedMLP(64, 128, norm=norm).cuda()
+    x = torch.empty(0, 64, dtype=BF, device="cuda", requires_grad=True)
+    out = m(x)
+    out.backward(torch.empty_like(out))
+    assert out.shape == (0, 64) and x.grad.shape == (0, 64)
+    assert all(p.grad.shape == p.shape and not p.grad.any() for p in m.parameters())
