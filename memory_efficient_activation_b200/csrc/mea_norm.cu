@@ -902,31 +902,32 @@ norm_bwd_ring_kernel(const void *x, const void *dy, const void *__restrict__ gam
     };
     V view(r0, C, SR, slot, g);
     const int row_hop = (int)(S * C);              // elements between a thread's rows of one stage
-    int64_t row = r0 + slot;
-    const int64_t at0 = (row * C + g * VL) * eb, hop = (int64_t)SR * C * eb, rh = (int64_t)row_hop * eb;
+    const int64_t at0 = ((r0 + slot) * C + g * VL) * eb, hop = (int64_t)SR * C * eb, rh = (int64_t)row_hop * eb;
     unsigned char *op = static_cast<unsigned char *>(dx) + at0;
     float mean_n[R], is_n[R];                      // statistics of the next stage's rows
-    auto stats = [&](int64_t from) {
+    const float *mp = RMS ? nullptr : mean_in + r0, *ip = invstd_in + r0;
+    const int count = (int)(r1 - r0);              // rows of the slab (below 0 past the end); at: this thread's next
+    int at = slot;
+    auto stats = [&] {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t at = from + r * S;
-            mean_n[r] = RMS || at >= r1 ? 0.f : mean_in[at];
-            is_n[r] = at >= r1 ? 0.f : invstd_in[at];
+        for (int r = 0; r < R; ++r, at += S) {
+            mean_n[r] = RMS || at >= count ? 0.f : mp[at];
+            is_n[r] = at >= count ? 0.f : ip[at];
         }
     };
-    stats(row);
-    int left = row < r1 ? (int)((r1 - row + S - 1) / S) : 0;   // rows of this slot still to come
+    stats();
+    int left = slot < count ? (count - slot + S - 1) / S : 0;   // rows of this slot still to come
     int st = 0;
     uint32_t turn = 0;
-    for (int s = 0; s < steps; ++s, row += SR, op += hop) {
+    for (int s = 0; s < steps; ++s, op += hop) {
         float mean[R], is[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mean[r] = mean_n[r];
             is[r] = is_n[r];
         }
-        if (!mbar_wait(smem_addr(full + st), turn)) atomicExch(&g_norm_error, 1u);
-        stats(row + SR);
+        if (!mbar_wait(smem_addr(full) + 8 * st, turn)) atomicExch(&g_norm_error, 1u);
+        stats();
         const unsigned char *sx = ring + st * 2 * kBytes, *sd = sx + kBytes;
         const int live = left < R ? left : R;      // this slot's rows in the stage
         left = left < R ? 0 : left - R;
