@@ -25,10 +25,10 @@
 //   longer rows, unaligned tensors    column sums, then dx
 //
 // Measured, 16384 x 4096 bf16 with fp32 parameters: forward 45 us (5.9 TB/s),
-// backward 81 us (5.0 TB/s) with dgamma and dbeta, 74 without.  What bounds
-// the backward is latency at 16 warps per SM: 181 instructions a warp and 256
-// elements issue in 55 percent of the cycles, two blocks of 64 registers (and
-// two rows between barriers) were slower.
+// backward 75 us (5.4 TB/s) and 4 to 6 more for the join of dgamma and dbeta.
+// What bounds the backward is latency at 16 warps per SM: 170 instructions a
+// warp and 256 elements issue in 57 percent of the cycles; two blocks of 64
+// registers (and two rows between barriers) were slower.
 #include <cuda_runtime.h>
 
 #include <cstdint>
