@@ -375,12 +375,7 @@ cudaError_t launch_few_one(const GatedLaunch &g)
     int ks = 1;
     while (ks < 4 * per_sm && tiles * ks * 2 <= (int64_t)kB200Sms * per_sm && kb >= ks * 2 * 4) ks *= 2;
     const uint32_t budget = (uint32_t)kFewSmemMax / per_sm - 2048;
-    // Four stages are enough beside a second CTA; a fifth for 16 tokens would
-    // only keep the next kernel's blocks off the SM (one token, 4096 to 2 x
-    // 8192: 24.6 -> 23.9 us back to back, norm and down projection along with
-    // it 41.2 -> 39.3).
-    const int most = per_sm == 2 ? 4 : 8;
-    a.stages = (int)(budget / stage) < most ? (int)(budget / stage) : most;
+    a.stages = (int)(budget / stage) < 8 ? (int)(budget / stage) : 8;
     a.tmem_cols = 32;
     while (a.tmem_cols < (uint32_t)a.mt) a.tmem_cols *= 2;
     const size_t part = (size_t)kRowsW * a.mt * sizeof(float);
