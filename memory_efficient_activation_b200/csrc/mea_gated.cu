@@ -108,10 +108,10 @@ struct Shape {
     static_assert(kSmemBytes <= 232448, "shared memory of a block");
 };
 
-// Instruction descriptor (kind::f16): fp32 accumulator, A and B bf16, N 256,
-// M 256; A K-major or M-major (bit 15), B K-major or N-major (bit 16).
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kAcc >> 3) << 17) |
-                            ((uint32_t)(kBM >> 4) << 24);
+// Instruction descriptor (kind::f16): fp32 accumulator, A and B bf16, M 256;
+// A K-major or M-major (bit 15), B K-major or N-major (bit 16), N / 8 from bit
+// 17 on.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kBM >> 4) << 24);
 
 __device__ __forceinline__ void record_error() { atomicExch(&g_gated_error, 1u); }
 
@@ -359,7 +359,7 @@ struct Maps {
 
 template <class A, Mode MODE, int EW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE, EW>::kThreads, 1)
-gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param, int want01, int want2)
+gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, int tw, float param, int want01, int want2)
 {
     using S = Shape<MODE, EW>;
     constexpr int kTN = S::kTN, kStages = S::kStages;
@@ -378,7 +378,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();          // 0: issues the MMAs of the pair
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int tiles_m = (M + kBM - 1) / kBM, tiles_n = (N + kTN - 1) / kTN;
+    const int tiles_m = (M + kBM - 1) / kBM, tiles_n = (N + tw - 1) / tw;
     const int ntiles = tiles_m * tiles_n;
     const int kblocks = (K + kBK - 1) / kBK;
 
@@ -446,9 +446,9 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                         tma_load_2d_pair(sa, &maps.x, kb * kBK, ra, fb);
                     }
                     if constexpr (MODE == kFwd) {
-                        tma_load_2d_pair(sb, rank == 0 ? &maps.w0 : &maps.w1, kb * kBK, tn * kTN, fb);
+                        tma_load_2d_pair(sb, rank == 0 ? &maps.w0 : &maps.w1, kb * kBK, tn * tw, fb);
                     } else {
-                        const int c = tn * kTN + rank * kHalf;
+                        const int c = tn * tw + (int)rank * (tw / 2);
                         if constexpr (S::kNMajorB) {
                             tma_load_2d_pair(sb, &maps.w0, c, kb * kBK, fb);
                             tma_load_2d_pair(sb + kStageA / 2, &maps.w0, c + 64, kb * kBK, fb);
@@ -467,6 +467,8 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
         if (lane == 0 && rank == 0) {
             int it = 0, lt = 0;
             bool ok = true;
+            const uint32_t idesc = kIdesc | (S::kMMajorA ? 1u << 15 : 0u) | (S::kNMajorB ? 1u << 16 : 0u) |
+                                   ((uint32_t)((MODE == kFwd ? 2 * tw : tw) >> 3) << 17);
             for (int t = pair; t < ntiles && ok; t += npairs, ++lt) {
                 const int b = lt & 1, use = lt >> 1;
                 if (use > 0 && !mbar_wait(smem_addr(acc_empty + b), (use & 1) ^ 1)) {
@@ -486,7 +488,6 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                     const uint32_t sa = sbase + s * kStageBytes, sb = sa + kStageA;
 #pragma unroll
                     for (int k = 0; k < kBK / kUmmaK; ++k) {
-                        constexpr uint32_t idesc = kIdesc | (S::kMMajorA ? 1u << 15 : 0u) | (S::kNMajorB ? 1u << 16 : 0u);
                         const uint64_t da = S::kMMajorA ? sdesc_mn(sa + k * kUmmaK * 128) : sdesc_sw128(sa + k * kUmmaK * 2);
                         const uint64_t db = S::kNMajorB ? sdesc_mn(sb + k * kUmmaK * 128) : sdesc_sw128(sb + k * kUmmaK * 2);
                         umma_bf16_pair(d, da, db, idesc, (kb | k) != 0);
@@ -524,8 +525,8 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
             tile_of<S::kGroupM>(t, tiles_m, tiles_n, tm, tn);
             Place p;
             p.row = tm * kBM + row_in;
-            p.col = tn * kTN + c0 * 32;
-            const int left = (N - p.col + 31) / 32;
+            p.col = tn * tw + c0 * 32;
+            const int end = tn * tw + tw < N ? tn * tw + tw : N, left = (end - p.col + 31) / 32;
             p.nc = p.row >= M || left < 0 ? 0 : left < kMost ? left : kMost;
             return p;
         };
@@ -579,7 +580,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, float param
                 const uint32_t buf = mine + (MODE == kBwd ? 2 * kIn : n % S::kOut) * kChunk;
                 if constexpr (MODE == kFwd) {
                     uint32_t u[32];
-                    tmem_ld32(lanes + kHalf + (c0 + c) * 32, u);
+                    tmem_ld32(lanes + tw + (c0 + c) * 32, u);
                     if (lane == 0) store_wait_read<S::kOut - 1>();
                     __syncwarp();
                     if (want01) {
@@ -656,14 +657,14 @@ bool chunk_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, i
 }
 
 template <class A, Mode MODE, int EW>
-cudaError_t launch_warps(const GatedLaunch &a, const Maps &m, int pairs)
+cudaError_t launch_warps(const GatedLaunch &a, const Maps &m, int tw, int pairs)
 {
     using S = Shape<MODE, EW>;
     auto kernel = gated_kernel<A, MODE, EW>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmemBytes);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3((unsigned)(2 * pairs)), dim3(S::kThreads), S::kSmemBytes, a.stream, m, (int)a.M,
-                      (int)a.N, (int)a.K, a.param, (int)(a.z != nullptr), (int)(a.h != nullptr));
+                      (int)a.N, (int)a.K, tw, a.param, (int)(a.z != nullptr), (int)(a.h != nullptr));
 }
 
 template <class A, Mode MODE>
@@ -688,14 +689,24 @@ cudaError_t launch_one(const GatedLaunch &a)
         ok = ok && chunk_map(&m.out0, z, a.M, a.N, a.N);
     }
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t tiles = ((a.M + kBM - 1) / kBM) * ((a.N + S::kTN - 1) / S::kTN);
+    // Tiles of 224 columns instead of 256 where they take fewer columns in
+    // rounds of all pairs (G^T h of 2048 x 5464 and 4096 tokens: 176 tiles are
+    // three rounds of 256, 200 three of 224: 89 -> 86 us; the backward [1023 x
+    // 2728 x 1024], one round either way, 17.8 -> 16.3).  The operand's tile in
+    // shared memory keeps its size, its last columns are loaded for nothing.
+    // Not in the forward, where 112 hidden units took as long as 128: loads
+    // out of L2 bound it there.
     const int pairs = sm_count() / 2;
+    const int64_t rows = (a.M + kBM - 1) / kBM;
+    auto cost = [&](int64_t w) { return (rows * ((a.N + w - 1) / w) + pairs - 1) / pairs * w; };
+    const int tw = MODE != kFwd && cost(S::kTN - 32) < cost(S::kTN) ? S::kTN - 32 : S::kTN;
+    const int64_t tiles = rows * ((a.N + tw - 1) / tw);
     // The forward and the plain products, whose epilogue does little, gained
     // nothing from eight warps; the backward 5 to 12 percent ([1023 x 2728 x
     // 1024] 18.7 -> 17.7 us, [300 x 2048 x 512] 14.9 -> 13.1).
     if constexpr (MODE == kBwd)
-        if (tiles <= pairs) return launch_warps<A, MODE, 8>(a, m, (int)tiles);
-    return launch_warps<A, MODE, 4>(a, m, (int)(tiles < pairs ? tiles : pairs));
+        if (tiles <= pairs) return launch_warps<A, MODE, 8>(a, m, tw, (int)tiles);
+    return launch_warps<A, MODE, 4>(a, m, tw, (int)(tiles < pairs ? tiles : pairs));
 }
 
 template <Mode MODE>
