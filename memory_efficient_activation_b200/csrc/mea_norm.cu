@@ -550,7 +550,10 @@ norm_fwd_ring_kernel(const void *__restrict__ x, const void *__restrict__ gamma,
 #pragma unroll
                 for (int off = 4; off >= 1; off >>= 1) u += __shfl_xor_sync(0xffffffffu, u, off);
                 mean = __shfl_sync(0xffffffffu, u, 0) * rc;
-                v = fmaf((mw - mean) * (mw - mean), nl, qw);
+                // a lane without a warp adds nothing: its own 0 - mean squared
+                // may overflow, and infinity times nl = 0 is no zero
+                const float d = nl > 0.f ? mw - mean : 0.f;
+                v = fmaf(d * d, nl, qw);
             }
 #pragma unroll
             for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);

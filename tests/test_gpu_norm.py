@@ -238,3 +238,19 @@ def test_norm_modules(cls, dtype):
     x.grad = None
     m(x).backward(torch.ones_like(x))
     assert m.gamma.grad is None and x.grad is not None
+
+
+@pytest.mark.parametrize("dtype,rows,C", [("f32", 1100, 1001), ("bf16", 2200, 1001), ("bf16", 500, 5120),
+                                          ("bf16", 200, 12288), ("f32", 300, 5120), ("bf16", 2500, 1024),
+                                          ("bf16", 20, 1001), ("f32", 20, 4096)])
+def test_norm_means_whose_square_overflows(dtype, rows, C):
+    """Means beyond 1.85e19 beside deviations whose squares are finite: rows of
+    two to seven warps in the streaming kernel, and the other kernels."""
+    x, _, gamma, beta = _inputs(rows, C, dtype, "f32", rows + C)
+    x[1::3] = (x[1::3].float() * 1e17 + 3e19).to(x.dtype)
+    x[2::3] = (x[2::3].float() * 1e16 - 2.5e19).to(x.dtype)
+    got = mea.norm_fwd("layer", x, gamma, beta)
+    want = ref.norm_fwd("layer", x, gamma, beta, 1e-5)
+    bounds = ref.norm_fwd_bounds("layer", x, gamma, beta, 1e-5, x.dtype)
+    for name, g, w, b in zip(("y", "mean", "invstd"), got, want, bounds):
+        ref.assert_within(g, w, b, name)
