@@ -226,14 +226,16 @@ struct Both {
         df = pk(A::template df<false>(x0, 1.f, k, tail), A::template df<false>(x1, 1.f, k, tail));
     }
 };
-// s = 1 / (1 + E), E = 2^t: f = x s, f' = s (1 + alpha x E s), E s = Sigmoid(-alpha x).
+// s = 1 / (1 + E), E = 2^t: f = x s, f' = s (1 + alpha x E s), E s = Sigmoid(-alpha x);
+// alpha x is limited as in df, so that an infinite one times E = 0 stays 0.
 template <bool RC>
 struct Both<SwishT<RC>> {
     static __device__ __forceinline__ void eval(float x0, float x1, const Coef &k, bool &tail, F2 &f, F2 &df)
     {
         const F2 x = pk(x0, x1);
-        float t0, t1, a0, a1;
+        float t0, t1, a0, a1, z0, z1;
         upk(mul2(x, sp2(k.c_hi)), t0, t1);
+        upk(mul2(x, sp2(k.p)), z0, z1);
         const F2 E = pk(ex2_ftz(t0), ex2_ftz(t1));
         tail |= fmaxf(t0, t1) > kTailT;
         if constexpr (RC)
@@ -242,7 +244,7 @@ struct Both<SwishT<RC>> {
         upk(add2(E, sp2(1.f)), a0, a1);
         const F2 s = pk(rcp_ftz(a0), rcp_ftz(a1));
         f = mul2(x, s);
-        df = mul2(s, fma2(mul2(x, sp2(k.p)), mul2(E, s), sp2(1.f)));
+        df = mul2(s, fma2(pk(fminf(z0, kBig), fminf(z1, kBig)), mul2(E, s), sp2(1.f)));
     }
 };
 // The same with t a cubic and x v' for alpha x (x beyond 2e10 in size, where

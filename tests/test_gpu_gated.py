@@ -347,3 +347,23 @@ def test_gated_block_of_no_tokens(norm):
     out.backward(torch.empty_like(out))
     assert out.shape == (0, 64) and x.grad.shape == (0, 64)
     assert all(p.grad.shape == p.shape and not p.grad.any() for p in m.parameters())
+
+
+@pytest.mark.parametrize("K", [72, 1288])
+@pytest.mark.parametrize("alpha", [1.0, 1.25, 2.0, -2.0, 0.0])
+def test_gated_bwd_swish_of_the_largest_gates(alpha, K):
+    """alpha times the gate overflows fp32 or is infinite: f' is 1 or 0 there
+    (as it is at 1e30 already), in the 256-row and in the few-token kernel.
+    Where alpha times the gate is no number (0 times infinity) neither is f'."""
+    g = _gen(17)
+    M, N = 40, 264
+    dout, wd = _normal(g, M, K), _normal(g, K, N, scale=K ** -0.5)
+    far = torch.tensor([1e30, 1e37, 3e38, float("inf"), 2.0], device="cuda")
+    gate = torch.cat([far, -far, far[:3]]).repeat(M * N // 13 + 1)[:M * N].view(M, N)
+    up = torch.ones(M, N, device="cuda")
+    dz, _ = mea.matmul_gated_act_bwd("swish", dout, wd, torch.cat([gate, up], 1).to(BF), alpha)
+    z = torch.cat([gate.clamp(-1e30, 1e30), up], 1).to(BF)
+    want, bound = ref.gated_bwd("swish", dout, wd, z, alpha)[0][:, :N], ref.gated_bwd_bounds("swish", dout, wd, z, alpha)[0][:, :N]
+    number = ~(alpha * gate).isnan()
+    ref.assert_within(dz[:, :N][number], want[number], bound[number], "d gate")
+    assert dz[:, :N][~number].isnan().all()
