@@ -1161,6 +1161,14 @@ class MemoryEfficientRMSNorm(MemoryEfficientLayerNorm):
         super().__init__(d_model, eps, bias=False, dtype=dtype)
 
 
+def _rows16(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and on a 16-byte boundary, as the tensor-core kernels read
+    it: a copy where it is not (a slice of a flat buffer, say, as the gradient
+    of a concatenation is one)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _gated_mlp(x, w_gate_up, w_down, gamma, beta, act, param, norm, eps, keep: bool):
     """The gated block's forward: (out, mean, invstd, z), z formed only where
     a backward will need it."""
@@ -1184,7 +1192,7 @@ class GatedMLPFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w_gate_up, w_down, gamma, beta, act: str, param: float, norm: str | None, eps: float):
-        x = x.contiguous()
+        x = _rows16(x)
         out, mean, invstd, z = _gated_mlp(x, w_gate_up, w_down, gamma, beta, act, param, norm, eps, True)
         ctx.args = (act, param, norm, eps)
         ctx.save_for_backward(x, w_gate_up, w_down, gamma, beta, mean, invstd, z)
@@ -1196,7 +1204,7 @@ class GatedMLPFunction(torch.autograd.Function):
         x, w_gate_up, w_down, gamma, beta, mean, invstd, z = ctx.saved_tensors
         act, param, norm, eps = ctx.args
         need = ctx.needs_input_grad
-        dout = dout.contiguous()
+        dout = _rows16(dout)
         dz, h = matmul_gated_act_bwd(act, dout, w_down, z, param, want_h=need[2])
         dw_down = matmul(dout, h, trans_a=True) if need[2] else None
         del h
@@ -1247,7 +1255,7 @@ class MemoryEfficientGatedMLP(torch.nn.Module):
         if torch.is_grad_enabled():
             out = GatedMLPFunction.apply(x, *args)
         else:
-            out = _gated_mlp(x.contiguous(), *args, False)[0]
+            out = _gated_mlp(_rows16(x), *args, False)[0]
         return out.view(*shape[:-1], out.shape[-1])
 
 

@@ -367,3 +367,23 @@ def test_gated_bwd_swish_of_the_largest_gates(alpha, K):
     number = ~(alpha * gate).isnan()
     ref.assert_within(dz[:, :N][number], want[number], bound[number], "d gate")
     assert dz[:, :N][~number].isnan().all()
+
+
+@pytest.mark.parametrize("norm", [None, "rms"])
+def test_gated_block_of_slices_off_a_16_byte_boundary(norm):
+    """Input and gradient that start at odd elements of flat buffers (the
+    gradient as the backward of a concatenation hands it over)."""
+    torch.manual_seed(18)
+    m = mea.MemoryEfficientGatedMLP(64, 128, norm=norm).cuda()
+    x, g = torch.randn(7 * 64 + 1, device="cuda").to(BF), torch.randn(7 * 64 + 3, device="cuda").to(BF)
+    whole, flat = x[1:].view(7, 64).clone().requires_grad_(), x.clone().requires_grad_()
+    want = m(whole)
+    want.backward(g[3:].view(7, 64).clone())
+    grads = [p.grad for p in m.parameters()]
+    m.zero_grad()
+    out = m(flat[1:].view(7, 64))
+    torch.cat([x[:3], out.flatten()]).backward(g)
+    assert torch.equal(out, want) and torch.equal(flat.grad[1:].view(7, 64), whole.grad)
+    assert all(torch.equal(p.grad, w) for p, w in zip(m.parameters(), grads))
+    with torch.no_grad():
+        assert torch.equal(m(x[1:].view(7, 64)), want)
