@@ -411,6 +411,7 @@ gated_kernel(const __grid_constant__ Maps maps, int M, int N, int K, int tw, flo
         mbar_init_fence();
     }
     if (warp == 1) {
+        __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");

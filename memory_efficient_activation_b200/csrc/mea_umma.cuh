@@ -69,8 +69,12 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+// The .aligned instructions below (cluster barriers, tensor-memory accesses)
+// are for a converged warp; after code that one lane runs alone, or a loop of
+// its own length per lane, __syncwarp makes it one.
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -105,6 +109,7 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // i of the warp receives lane (base lane + i), columns col .. col + 31.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
 {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
