@@ -85,6 +85,11 @@ struct Store<float> {
     {
         return __ldg(static_cast<const float *>(p) + i);
     }
+    // of a tensor that the kernel may also write: not by the read-only path
+    static __device__ __forceinline__ float load1_rw(const void *p, int64_t i)
+    {
+        return static_cast<const float *>(p)[i];
+    }
     static __device__ __forceinline__ void store1(void *p, int64_t i, float v)
     {
         static_cast<float *>(p)[i] = v;
@@ -114,6 +119,10 @@ struct Store<Bf16> {
     {
         uint16_t b = __ldg(static_cast<const unsigned short *>(p) + i);
         return __uint_as_float(static_cast<uint32_t>(b) << 16);
+    }
+    static __device__ __forceinline__ float load1_rw(const void *p, int64_t i)
+    {
+        return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
     }
     static __device__ __forceinline__ void store1(void *p, int64_t i, float v)
     {

@@ -68,16 +68,6 @@ inline int64_t norm_slabs(int64_t rows, int at_a_time)
     return s < 1 ? 1 : s;
 }
 
-// One element of a tensor that the kernel may also write (dx over x or dy).
-template <typename T>
-__device__ __forceinline__ float load1_rw(const void *p, int64_t i)
-{
-    if constexpr (Store<T>::kBytes == 2)
-        return __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16);
-    else
-        return static_cast<const float *>(p)[i];
-}
-
 // VL parameters from item i (elements i VL ..), or `fill` where p is NULL.
 template <typename TP, int VL>
 __device__ __forceinline__ void load_params(const void *p, int64_t i, float fill, float (&f)[VL])
@@ -268,7 +258,8 @@ struct RingView {
         const int64_t first = a & ~(int64_t)(q - 1);
         if (n) bulk_load(smem_addr(dst), static_cast<const unsigned char *>(p) + first * Store<T>::kBytes, n, bar);
         if constexpr (VL == 1)
-            for (int64_t i = first + n / Store<T>::kBytes; i < b; ++i) Store<T>::store1(dst, i - first, load1_rw<T>(p, i));
+            for (int64_t i = first + n / Store<T>::kBytes; i < b; ++i)
+                Store<T>::store1(dst, i - first, Store<T>::load1_rw(p, i));
     }
     uint32_t at;             // this thread's item 0: elements from the rows' start in the stage
     uint32_t skew, turn;     // VL 1: elements before the rows' start, and their change per step
@@ -287,7 +278,7 @@ struct RingView {
     __device__ __forceinline__ void load(const unsigned char *stage, int i, int off, float (&f)[VL]) const
     {
         if constexpr (VL == 1)
-            f[0] = load1_rw<T>(stage, skew + at + off + i);
+            f[0] = Store<T>::load1_rw(stage, skew + at + off + i);
         else
             Store<T>::unpack(*reinterpret_cast<const uint4 *>(stage + (at + off + i * VL) * Store<T>::kBytes), f);
     }
@@ -1081,9 +1072,9 @@ norm_dx_long_kernel(const void *x, const void *dy, const void *__restrict__ gamm
     double s1 = 0.0, s2 = 0.0;
     for (int64_t i = threadIdx.x; i < C; i += blockDim.x) {
         const float w = gamma ? Store<TP>::load1(gamma, i) : 1.f;
-        const float a = load1_rw<T>(dy, base + i) * w;
+        const float a = Store<T>::load1_rw(dy, base + i) * w;
         s1 += a;
-        s2 += a * ((load1_rw<T>(x, base + i) - mean) * is);
+        s2 += a * ((Store<T>::load1_rw(x, base + i) - mean) * is);
     }
     s1 = block_sum(s1, red);
     s2 = block_sum(s2, red);
@@ -1095,8 +1086,8 @@ norm_dx_long_kernel(const void *x, const void *dy, const void *__restrict__ gamm
     pdl_trigger();
     for (int64_t i = threadIdx.x; i < C; i += blockDim.x) {
         const float w = gamma ? Store<TP>::load1(gamma, i) : 1.f;
-        const float xh = (load1_rw<T>(x, base + i) - mean) * is;
-        Store<T>::store1(dx, base + i, is * (fmaf(-xh, bc[1], load1_rw<T>(dy, base + i) * w) - bc[0]));
+        const float xh = (Store<T>::load1_rw(x, base + i) - mean) * is;
+        Store<T>::store1(dx, base + i, is * (fmaf(-xh, bc[1], Store<T>::load1_rw(dy, base + i) * w) - bc[0]));
     }
 }
 

@@ -43,10 +43,11 @@ struct Item {
             return ld_nc_v4(static_cast<const uint4 *>(p) + i);
         }
     }
+    // Of a tensor that the kernel may also write (an output over its input).
     static __device__ __forceinline__ Raw load_rw(const void *p, int64_t i)
     {
         if constexpr (VL == 1) {
-            return Store<T>::load1(p, i);
+            return Store<T>::load1_rw(p, i);
         } else {
             return *(static_cast<const uint4 *>(p) + i);
         }

@@ -254,3 +254,23 @@ def test_norm_means_whose_square_overflows(dtype, rows, C):
     bounds = ref.norm_fwd_bounds("layer", x, gamma, beta, 1e-5, x.dtype)
     for name, g, w, b in zip(("y", "mean", "invstd"), got, want, bounds):
         ref.assert_within(g, w, b, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("rows,C", [(700, 272), (64, 1001), (3, 20000)])
+def test_norm_dx_in_place_unaligned(rows, C, norm, dtype):
+    """dx over x and over dy, single elements of tensors off a 16-byte
+    boundary."""
+    def fresh():
+        x, dy, gamma, _ = _inputs(rows, C, dtype, "f32", rows + C, offset=1)
+        assert x.data_ptr() % 16 and dy.data_ptr() % 16
+        return x, dy, gamma
+
+    x, dy, gamma = fresh()
+    mean, invstd = mea.norm_fwd(norm, x, gamma)[1:]
+    first = mea.norm_bwd(norm, x, dy, gamma, mean, invstd, want_dbeta=True, out=fresh()[0])
+    for target in ("x", "dy"):
+        x, dy, gamma = fresh()
+        got = mea.norm_bwd(norm, x, dy, gamma, mean, invstd, want_dbeta=True, out=x if target == "x" else dy)
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
