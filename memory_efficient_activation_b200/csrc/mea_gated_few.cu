@@ -384,8 +384,13 @@ cudaError_t launch_few_one(const GatedLaunch &g)
     size_t smem = (size_t)a.stages * stage;
     if (smem < part) smem = part;
     smem += 1024;
+    // the gated backward and a transposed A come here for a share of K only
+    // (at most 74 tiles of this width, 20 K blocks or more)
+    constexpr bool kShared = (!std::is_same<A, void>::value && WN) || XM;
     switch (ks) {
-    case 1: return launch_ks<A, 1, WN, XM>(a, tiles, smem, g.stream);
+    case 1:
+        if constexpr (!kShared) return launch_ks<A, 1, WN, XM>(a, tiles, smem, g.stream);
+        return cudaErrorInvalidValue;
     case 2: return launch_ks<A, 2, WN, XM>(a, tiles, smem, g.stream);
     case 4: return launch_ks<A, 4, WN, XM>(a, tiles, smem, g.stream);
     }

@@ -1188,15 +1188,14 @@ bool fwd_warp(const NormLaunch &a, cudaError_t *e)
     constexpr int kParam = Store<T>::V * Store<TP>::kBytes * 2 < 16 ? 16 : Store<T>::V * Store<TP>::kBytes * 2;
     int nv = 2;
     while (nv * 32 < items) nv <<= 1;
-    *e = by_nv(nv, [&](auto n) -> cudaError_t {
-        auto kernel = norm_fwd_warp_kernel<T, TP, RMS, decltype(n)::value>;
-        const size_t smem = (size_t)items * kParam;
-        if (smem > 48 * 1024) {
-            cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (s != cudaSuccess) return s;
-        }
-        return launch_pdl(kernel, dim3((unsigned)grid), dim3(kWarpThreads), smem, a.stream, a.x, a.gamma, a.beta, a.eps,
-                          a.out, a.mean, a.invstd, a.rows, a.C);
+    *e = by_nv(nv, [&](auto n) -> cudaError_t {    // 2 to 16; 512 vectors' parameters are 32 KB
+        constexpr int NV = decltype(n)::value;
+        if constexpr (NV == 1)
+            return cudaErrorInvalidValue;
+        else
+            return launch_pdl(norm_fwd_warp_kernel<T, TP, RMS, NV>, dim3((unsigned)grid), dim3(kWarpThreads),
+                              (size_t)items * kParam, a.stream, a.x, a.gamma, a.beta, a.eps, a.out, a.mean, a.invstd,
+                              a.rows, a.C);
     });
     return true;
 }
@@ -1216,12 +1215,22 @@ cudaError_t fwd_vl(const NormLaunch &a)
                           a.x, a.gamma, a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C);
     const int threads = (1 << g.lg) > kNormThreads ? (1 << g.lg) : kNormThreads;
     const int64_t per = threads >> g.lg;
-    return by_nv(g.nv, [&](auto nv) {
+    // Vectors: 2 to 8 a thread are asked for by tensors that the kernels above
+    // take, unless the row fills 1024 threads; 16 by bf16 rows of 2049 to 4096
+    // vectors in blocks of 256 alone (fp32 rows as long are the ring's).
+    constexpr bool kVec = VL > 1;
+    return by_nv(g.nv, [&](auto nv) -> cudaError_t {
         constexpr int NV = decltype(nv)::value;
-        auto kernel = threads > kNormThreads ? norm_fwd_kernel<T, TP, RMS, VL, NV, kNormMaxThreads>
-                                             : norm_fwd_kernel<T, TP, RMS, VL, NV, kNormThreads>;
-        return launch_pdl(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads), 0, a.stream, a.x, a.gamma,
-                          a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C, g.lg);
+        constexpr bool kWide = !kVec || NV <= 8, kNarrow = !kVec || NV == 1 || (NV == 16 && VL == 8);
+        auto launch = [&](auto kernel) {
+            return launch_pdl(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads), 0, a.stream, a.x,
+                              a.gamma, a.beta, a.eps, a.out, a.mean, a.invstd, a.rows, a.C, g.lg);
+        };
+        if constexpr (kWide)
+            if (threads > kNormThreads) return launch(norm_fwd_kernel<T, TP, RMS, VL, NV, kNormMaxThreads>);
+        if constexpr (kNarrow)
+            if (threads == kNormThreads) return launch(norm_fwd_kernel<T, TP, RMS, VL, NV, kNormThreads>);
+        return cudaErrorInvalidValue;
     });
 }
 
@@ -1263,7 +1272,9 @@ bool bwd_ring(const NormLaunch &a, cudaError_t *e)
 template <typename T, typename TP, bool RMS, int VL>
 cudaError_t bwd_vl(const NormLaunch &a)
 {
-    constexpr int kMost = VL == 1 ? 16 : 4;        // items per thread of two tensors, in 64 registers
+    // items per thread of two tensors, in 64 registers; vectors: rows that the
+    // ring does not hold give each of 1024 threads three or four
+    constexpr int kMost = VL == 1 ? 16 : 4, kLeast = VL == 1 ? 1 : 4;
     cudaError_t fe;
     if (bwd_ring<T, TP, RMS, VL>(a, &fe)) return fe;
     if (a.dgamma || a.dbeta) {
@@ -1285,10 +1296,11 @@ cudaError_t bwd_vl(const NormLaunch &a)
     const int threads = (1 << g.lg) > kNormThreads ? (1 << g.lg) : kNormThreads;
     const int64_t per = threads >> g.lg;
     return by_nv(g.nv, [&](auto nv) -> cudaError_t {
-        if constexpr (decltype(nv)::value > kMost)
+        constexpr int NV = decltype(nv)::value;
+        if constexpr (NV < kLeast || NV > kMost)
             return cudaErrorInvalidValue;
         else
-            return launch_pdl(norm_dx_kernel<T, TP, RMS, VL, decltype(nv)::value>,
+            return launch_pdl(norm_dx_kernel<T, TP, RMS, VL, NV>,
                               dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads), 0, a.stream, a.x, a.dy,
                               a.gamma, a.mean_in, a.invstd_in, a.out, a.rows, a.C, g.lg);
     });

@@ -274,3 +274,23 @@ def test_norm_dx_in_place_unaligned(rows, C, norm, dtype):
         x, dy, gamma = fresh()
         got = mea.norm_bwd(norm, x, dy, gamma, mean, invstd, want_dbeta=True, out=x if target == "x" else dy)
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_either_side_of_the_kernels_borders(dtype):
+    """Sizes around every border between the kernels and between their numbers
+    of items per thread: rows of one to more than 1024 threads' worth, few rows
+    and enough to stream, whole vectors and single elements."""
+    V = 8 if dtype == "bf16" else 4
+    shapes = []
+    for items in (1, 2, 32, 33, 64, 65, 128, 129, 256, 257, 512, 513, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193):
+        small, large = max(1, (3 << 20) // (16 * items)), (5 << 20) // (16 * items)
+        shapes += [(r, items * V) for r in (1, min(small, 3000), min(large, 6000))]
+        if items > 4000:
+            shapes += [(2400, items * V)]
+    for C in (1, 3, 31, 33, 257, 511, 513, 1025, 2047, 2049, 4097, 8191, 8193, 16385):
+        shapes += [(1, C), (max(1, min(3000, (1 << 20) // C)), C), (min(6000, (3 << 20) // C), C)]
+    for rows, C in shapes:
+        x, dy, gamma, beta = _inputs(rows, C, dtype, "f32", rows + C)
+        for norm in NORMS:
+            _check(norm, x, dy, gamma, beta)
