@@ -692,17 +692,20 @@ cudaError_t launch_one(const GatedLaunch &a)
         ok = ok && chunk_map(&m.out0, z, a.M, a.N, a.N);
     }
     if (!ok) return cudaErrorInvalidValue;
-    // Tiles of 224 columns instead of 256 where they take fewer columns in
-    // rounds of all pairs (G^T h of 2048 x 5464 and 4096 tokens: 176 tiles are
-    // three rounds of 256, 200 three of 224: 89 -> 86 us; the backward [1023 x
-    // 2728 x 1024], one round either way, 17.8 -> 16.3).  The operand's tile in
-    // shared memory keeps its size, its last columns are loaded for nothing.
+    // Tiles of 224 columns instead of 256 where they take no more rounds of all
+    // pairs (us back to back, 224 / 256: plain [1024 x 1024 x 1024] 8.5 / 9.0,
+    // G^T h of 2048 x 5464 and 4096 tokens, three rounds, 71 / 75; the backward
+    // [1023 x 2728 x 1024] 15.7 / 17.1, [1024 x 1024 x 1024] 13.9 / 15.2).
+    // With a round more they lose, although its columns are fewer: the operands
+    // are read more often ([8192 x 5464 x 1024], 11 rounds against 10, plain 86 /
+    // 76, backward 173 / 171).  The operand's tile in shared memory keeps its
+    // size, its last columns are loaded for nothing.
     // Not in the forward, where 112 hidden units took as long as 128: loads
     // out of L2 bound it there.
     const int pairs = sm_count() / 2;
     const int64_t rows = (a.M + kBM - 1) / kBM;
-    auto cost = [&](int64_t w) { return (rows * ((a.N + w - 1) / w) + pairs - 1) / pairs * w; };
-    const int tw = MODE != kFwd && cost(S::kTN - 32) < cost(S::kTN) ? S::kTN - 32 : S::kTN;
+    auto rounds = [&](int64_t w) { return (rows * ((a.N + w - 1) / w) + pairs - 1) / pairs; };
+    const int tw = MODE != kFwd && rounds(S::kTN - 32) <= rounds(S::kTN) ? S::kTN - 32 : S::kTN;
     const int64_t tiles = rows * ((a.N + tw - 1) / tw);
     // The forward and the plain products, whose epilogue does little, gained
     // nothing from eight warps; the backward 5 to 12 percent ([1023 x 2728 x

@@ -387,3 +387,31 @@ def test_gated_block_of_slices_off_a_16_byte_boundary(norm):
     assert all(torch.equal(p.grad, w) for p, w in zip(m.parameters(), grads))
     with torch.no_grad():
         assert torch.equal(m(x[1:].view(7, 64)), want)
+
+
+def _matmul_check(ta, tb, M, N, K):
+    g = _gen(M + N + K)
+    a = _normal(g, *((K, M) if ta else (M, K)))
+    b = _normal(g, *((N, K) if tb else (K, N)))
+    c = mea.matmul(a, b, ta, tb)
+    A, B = a.t() if ta else a, b.t() if tb else b
+    want = A.double() @ B.double()
+    e = K * 2.0 ** -23 * (A.double().abs() @ B.double().abs())
+    ref.assert_within(c, want, e + 2.0 ** -8 * (want.abs() + e) + ref.TINY, "c")
+    ref.assert_close_overall(c, want, "c")
+    assert torch.equal(c, mea.matmul(a, b, ta, tb))
+
+
+WIDTHS = [(4096, 4096, 136), (2296, 2040, 200), (8192, 5464, 64),      # 256 columns: 224 would take a round more
+          (4096, 2736, 72), (2048, 5464, 72)]                          # 224 columns
+
+
+@pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("M,N,K", WIDTHS)
+def test_matmul_of_both_tile_widths(ta, tb, M, N, K):
+    _matmul_check(ta, tb, M, N, K)
+
+
+@pytest.mark.parametrize("M,N,K", WIDTHS)
+def test_gated_bwd_of_both_tile_widths(M, N, K):
+    _bwd("gelu_tanh", M, N, K, M + N)
