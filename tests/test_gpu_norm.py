@@ -294,3 +294,28 @@ def test_norm_either_side_of_the_kernels_borders(dtype):
         x, dy, gamma, beta = _inputs(rows, C, dtype, "f32", rows + C)
         for norm in NORMS:
             _check(norm, x, dy, gamma, beta)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("path", ["vectors", "odd width", "unaligned", "long rows"])
+@pytest.mark.parametrize("rows", [1, 147, 149, 1023, 1025, 2049, 40001, 151553, 303105])
+def test_norm_column_sums_count_every_row_once(rows, path, dtype):
+    """Mean 0, invstd 1, elements and gradients of -3, -1, 1 and 3: every term
+    is an odd integer and every partial sum below 2^24, so the sums are exact
+    in any order, and a row lost or taken twice changes each of them."""
+    C = {"vectors": 24, "odd width": 27, "unaligned": 24, "long rows": 16392 if dtype == "bf16" else 8200}[path]
+    if path == "long rows":
+        rows = min(rows, 2049)
+    assert 9 * rows < 1 << 24
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+
+    def odd():
+        buf = torch.empty(rows * C + 1, dtype=DT[dtype], device="cuda")[1 if path == "unaligned" else 0:][:rows * C]
+        return buf.view(rows, C).copy_(torch.randint(-2, 2, (rows, C), generator=gen, device="cuda") * 2 + 1)
+
+    x, dy = odd(), odd()
+    mean, invstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    for norm in NORMS:
+        _, dg, db = mea.norm_bwd(norm, x, dy, None, mean, invstd, want_dgamma=True, want_dbeta=True)
+        assert torch.equal(dg.double(), (x.double() * dy.double()).sum(0))
+        assert torch.equal(db.double(), dy.double().sum(0))
