@@ -415,3 +415,104 @@ def test_matmul_of_both_tile_widths(ta, tb, M, N, K):
 @pytest.mark.parametrize("M,N,K", WIDTHS)
 def test_gated_bwd_of_both_tile_widths(M, N, K):
     _bwd("gelu_tanh", M, N, K, M + N)
+
+
+# Sums of 20 K blocks (1217 terms) and more over few tiles: K shared out over a
+# cluster of two, four or eight blocks, one or two of them on an SM.
+
+@pytest.mark.parametrize("ta,tb", [(False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("M,N,K", [(8, 8, 1288), (1, 136, 4104), (128, 128, 8192), (200, 264, 6152), (264, 520, 1400),
+                                   (512, 1032, 2056), (40, 1032, 2049), (1032, 264, 4099), (2048, 1032, 3080)])
+def test_matmul_of_shared_sums(ta, tb, M, N, K):
+    _matmul_check(ta, tb, -(-M // 8) * 8 if ta else M, N, K if ta else K // 8 * 8)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", [(1, 264, 1288), (100, 264, 1288), (200, 520, 2056), (256, 136, 4104)])
+def test_gated_bwd_of_shared_sums(act, M, N, K):
+    dout, wd, z, dz, _ = _bwd(act, M, N, K, M + N + K)
+    zc = z.clone()
+    over, none = mea.matmul_gated_act_bwd(act, dout, wd, zc, _p(act), want_h=False, dz=zc)
+    assert over is zc and none is None and torch.equal(dz, zc)
+
+
+@pytest.mark.parametrize("act", ["swish", "gelu_tanh", "tanh"])
+@pytest.mark.parametrize("M,N,K", [(300, 264, 2056), (515, 520, 2056), (700, 256, 4104), (1030, 72, 1288)])
+def test_gated_fwd_of_shared_sums(act, M, N, K):
+    """Several tiles of tokens, the last of them cut short."""
+    a = _fwd(act, M, N, K, M + N)
+    assert torch.equal(a[4], _fwd(act, M, N, K, M + N, want_z=False)[4])
+
+
+@pytest.mark.parametrize("act,param", [(a, _p(a)) for a in ACTS] + [("swish", 1.0), ("swish", -0.7), ("swish", 0.0)])
+def test_gated_bwd_extreme_gates_of_shared_sums(act, param):
+    """As test_gated_bwd_extreme_gates, through the other epilogue."""
+    g = _gen(19)
+    M, N, K = 40, 264, 1288
+    dout, wd = _normal(g, M, K), _normal(g, K, N, scale=K ** -0.5)
+    gate = torch.empty(M, N, device="cuda")
+    gate[:20] = torch.linspace(-1.6, -0.6, 20 * N, device="cuda").view(20, N)
+    far = torch.tensor([0.0, 5.0, 12.0, 13.5, 20.0, 60.0, 88.0, 100.0, 1e3, 1e6, 1e15, 1e30], device="cuda")
+    gate[20:] = torch.cat([far, -far]).repeat(20 * N // 24)[:20 * N].view(20, N)
+    z = torch.cat([gate, torch.ones(M, N, device="cuda")], 1).to(BF)
+    dz, h = mea.matmul_gated_act_bwd(act, dout, wd, z, param)
+    rdz, rh = ref.gated_bwd(act, dout, wd, z, param)
+    bdz, bh = ref.gated_bwd_bounds(act, dout, wd, z, param)
+    ref.assert_within(dz, rdz, bdz, "dz")
+    ref.assert_within(h, rh, bh, "h")
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 136, 1288), (131, 136, 1288), (259, 72, 1288)])
+def test_shared_sums_write_nothing_beyond_their_outputs(M, N, K):
+    def guarded(rows, cols):
+        buf = torch.full((rows * cols + 128,), 7.0, dtype=BF, device="cuda")
+        return buf, buf[64:64 + rows * cols].view(rows, cols)
+
+    g = _gen(20)
+    x, wg, wu, wd, z0 = _normal(g, M, K), _normal(g, N, K), _normal(g, N, K), _normal(g, K, N), _normal(g, M, 2 * N)
+    bufs = [guarded(M, 2 * N), guarded(M, N), guarded(M, 2 * N), guarded(M, N), guarded(M, N), guarded(136, 264)]
+    mea.matmul_gated_act_fwd("swish", x, wg, wu, z=bufs[0][1], h=bufs[1][1])
+    mea.matmul_gated_act_bwd("swish", x, wd, z0, dz=bufs[2][1], h=bufs[3][1])
+    mea.matmul(x, wd, out=bufs[4][1])
+    mea.matmul(_normal(g, K, 136), _normal(g, K, 264), True, out=bufs[5][1])
+    for b, _ in bufs:
+        assert (b[:64] == 7).all() and (b[-64:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [2, 150, 300])
+def test_shared_sums_in_a_graph_and_on_two_streams(M):
+    g = _gen(21)
+    N, K = 136, 2056
+    x, wg, wu, wd, z0 = _normal(g, M, K), _normal(g, N, K), _normal(g, N, K), _normal(g, K, N), _normal(g, M, 2 * N)
+    a, b = _normal(g, K, 136), _normal(g, K, 264)
+
+    def step():
+        return (mea.matmul_gated_act_fwd("swish", x, wg, wu) + mea.matmul_gated_act_bwd("swish", x, wd, z0) +
+                (mea.matmul(x, wd), mea.matmul(x, wg, False, True), mea.matmul(a, b, True)))
+
+    want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(step())
+    torch.cuda.synchronize()
+    for o in [out] + outs:
+        assert all(torch.equal(p, q) for p, q in zip(o, want))
+
+
+@pytest.mark.parametrize("norm", [None, "layer", "rms"])
+@pytest.mark.parametrize("batch,D,H", [((2, 650), 64, 128), ((1, 40), 1288, 1400), ((5, 300), 1288, 136)])
+def test_gated_block_of_shared_sums(norm, batch, D, H):
+    """The block where the weights' gradients (many tokens of a small model)
+    or the projections (few tokens) share their sums."""
+    test_gated_block(norm, "swish", batch, D, H)
