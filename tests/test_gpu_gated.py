@@ -516,3 +516,26 @@ def test_gated_block_of_shared_sums(norm, batch, D, H):
     """The block where the weights' gradients (many tokens of a small model)
     or the projections (few tokens) share their sums."""
     test_gated_block(norm, "swish", batch, D, H)
+
+
+def test_gated_tensors_of_more_than_2_31_elements():
+    """The last rows of a large batch are those of a small one (every sum over
+    k has one order), and the last columns of a wide weight those of a narrow
+    one."""
+    g = _gen(22)
+    M, N, K, n = 140000, 8192, 64, 4096
+    x, wg, wu, wd = _normal(g, M, K), _normal(g, N, K), _normal(g, N, K), _normal(g, K, N)
+    z, h = mea.matmul_gated_act_fwd("swish", x, wg, wu)
+    zs, hs = mea.matmul_gated_act_fwd("swish", x[-n:], wg, wu)
+    assert z.numel() > 2 ** 31 and torch.equal(z[-n:], zs) and torch.equal(h[-n:], hs)
+    dz, hb = mea.matmul_gated_act_bwd("swish", x, wd, z, dz=z, h=h)
+    dzs, hbs = mea.matmul_gated_act_bwd("swish", x[-n:], wd, zs)
+    assert torch.equal(dz[-n:], dzs) and torch.equal(hb[-n:], hbs)
+    del z, dz, zs, dzs
+    M, N = 64, 1 << 24
+    x, wg, wu = _normal(g, M, 8), _normal(g, N + 64, 8), _normal(g, N + 64, 8)
+    z, h = mea.matmul_gated_act_fwd("swish", x, wg, wu)
+    n = 8192
+    zs, hs = mea.matmul_gated_act_fwd("swish", x, wg[-n:], wu[-n:])
+    assert z.numel() > 2 ** 31 and torch.equal(h[:, -n:], hs)
+    assert torch.equal(z[:, -n:], zs[:, n:]) and torch.equal(z[:, N + 64 - n:N + 64], zs[:, :n])

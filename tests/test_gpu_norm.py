@@ -319,3 +319,32 @@ def test_norm_column_sums_count_every_row_once(rows, path, dtype):
         _, dg, db = mea.norm_bwd(norm, x, dy, None, mean, invstd, want_dgamma=True, want_dbeta=True)
         assert torch.equal(dg.double(), (x.double() * dy.double()).sum(0))
         assert torch.equal(db.double(), dy.double().sum(0))
+
+
+@pytest.mark.parametrize("rows,C", [(300000, 8192), (2200000, 1001), (66000, 32776)])
+def test_norm_tensors_of_more_than_2_31_elements(rows, C):
+    """The last rows of a large tensor are those of a small one of the same
+    alignment, and the column sums count every row (exact integers)."""
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    x, dy = (torch.empty(rows, C, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for t in (x, dy):
+        t.random_(-2, 2, generator=gen).mul_(2).add_(1)
+    n = 8000
+    assert x.numel() > 2 ** 31
+    gamma = torch.randn(C, generator=gen, device="cuda")
+    y, mean, invstd = mea.norm_fwd("layer", x, gamma)
+    ys, ms, iss = mea.norm_fwd("layer", x[-n:].clone(), gamma)
+    assert torch.equal(y[-n:], ys) and torch.equal(mean[-n:], ms) and torch.equal(invstd[-n:], iss)
+    del y
+    dx, _, _ = mea.norm_bwd("layer", x, dy, gamma, mean, invstd)
+    dxs, _, _ = mea.norm_bwd("layer", x[-n:].clone(), dy[-n:].clone(), gamma, ms, iss)
+    assert torch.equal(dx[-n:], dxs)
+    del dx, dxs
+    one, zero = torch.ones(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    _, dg, db = mea.norm_bwd("layer", x, dy, None, zero, one, want_dgamma=True, want_dbeta=True)
+    eg, eb = torch.zeros(C, dtype=torch.double, device="cuda"), torch.zeros(C, dtype=torch.double, device="cuda")
+    for i in range(0, rows, 20000):
+        a, b = x[i:i + 20000].float(), dy[i:i + 20000].float()
+        eg += (a * b).sum(0, dtype=torch.double)
+        eb += b.sum(0, dtype=torch.double)
+    assert torch.equal(dg.double(), eg.float().double()) and torch.equal(db.double(), eb)
