@@ -44,8 +44,9 @@ typedef enum { MEA_LAYER_NORM = 0, MEA_RMS_NORM = 1 } mea_norm_t;
  *   y            device, [rows x C], written.
  *   mean, invstd device fp32 [rows], written; either may be NULL; mean is
  *                ignored for MEA_RMS_NORM.
- * Row statistics are fp32 sums (over long rows fp64), the variance a second
- * pass over the row; y is rounded once.  Outputs must not overlap an input
+ * Row statistics are fp32 sums (over long rows fp64), the variance sums of
+ * squared distances from the row's mean, or from the means of its parts and
+ * those merged; y is rounded once.  Outputs must not overlap an input
  * or each other.
  * Source: layer normalisation in its standard definition; the save-input-only
  * scheme of the Swish page applied to it (x and two floats per row are kept,
@@ -77,7 +78,9 @@ MEA_API size_t mea_norm_bwd_workspace_bytes(int64_t rows, int64_t C);
  *                contents (no counter, no zero-fill).  Calls that share it
  *                must not run concurrently on the GPU.
  * Column sums take at most 1024 rows in fp32 and add those sums in fp64, in
- * an order fixed by the shape. */
+ * an order fixed by the shape, the types and which pointers lie on 16-byte
+ * boundaries: the same call repeats its bits, the same values at another
+ * alignment may give others. */
 MEA_API mea_status_t mea_norm_bwd(mea_norm_t norm, mea_dtype_t dtype, mea_dtype_t param_dtype, int64_t rows,
                                   int64_t C, const void *x, const void *dy, const void *gamma, const float *mean,
                                   const float *invstd, void *dx, void *dgamma, void *dbeta, void *workspace,

@@ -33,14 +33,14 @@
 // over k in one fixed order.  Every barrier wait is bounded: one that expires
 // sets g_gated_error and the roles stop issuing work.
 //
-// Measured, bf16, swish, [8192 x 4096] and 8192 hidden units: forward with z
-// 660 us at full clocks (1.67 PFLOP/s; tensor pipe 93% active), 805-840 back to
-// back under the board's power limit (1.31-1.37, as a library's plain product
-// of that size there); backward 391-415 us (1.33-1.41 PFLOP/s, tensor pipe 75%
-// active).  What the backward lacks is L2 and shared-memory bandwidth: z, dz
-// and h are 10 bytes per element of an output that the operands' tiles already
-// stream 128 FLOP per byte for (without its stores 375 us, without loads,
-// stores and arithmetic 339).
+// Measured, bf16, swish, [8192 x 4096] and 8192 hidden units.  One launch at
+// full clocks: forward with z 687 us (1.60 PFLOP/s; tensor pipe 90% active),
+// backward 390 (1.41; 75%).  Back to back, under the board's power limit:
+// forward 785-815 (1.35-1.40, as a library's plain product of that size
+// there), backward 465-500 (1.10-1.18).  What the backward lacks is L2 and
+// shared-memory bandwidth: z, dz and h are 10 bytes per element of an output
+// that the operands' tiles already stream 128 FLOP per byte for (without its
+// stores 375 us, without loads, stores and arithmetic 339, one launch each).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -708,8 +708,8 @@ cudaError_t launch_one(const GatedLaunch &a)
     const int tw = MODE != kFwd && rounds(S::kTN - 32) <= rounds(S::kTN) ? S::kTN - 32 : S::kTN;
     const int64_t tiles = rows * ((a.N + tw - 1) / tw);
     // The forward and the plain products, whose epilogue does little, gained
-    // nothing from eight warps; the backward 5 to 12 percent ([1023 x 2728 x
-    // 1024] 18.7 -> 17.7 us, [300 x 2048 x 512] 14.9 -> 13.1).
+    // nothing from eight warps; the backward 7 to 14 percent (back to back,
+    // [1023 x 2728 x 1024] 16.9 -> 15.7 us, [300 x 2048 x 512] 13.6 -> 11.7).
     if constexpr (MODE == kBwd)
         if (tiles <= pairs) return launch_warps<A, MODE, 8>(a, m, tw, (int)tiles);
     return launch_warps<A, MODE, 4>(a, m, tw, (int)(tiles < pairs ? tiles : pairs));

@@ -10,7 +10,8 @@
 //
 // Both are bound by memory (8 to 14 operations per element), so each tensor is
 // read once.  The variance is a second pass over the row on chip (sum of (x -
-// mean)^2), not a difference of two large sums.  Row sums are fp32, short
+// mean)^2; in the forward's ring over each warp's part of it from that part's
+// mean, the parts merged), not a difference of two large sums.  Row sums are fp32, short
 // sequences in a thread and then a tree; column sums take at most 1024 rows in
 // fp32 and add those in fp64.  Every kernel's results are rounded once.
 //
@@ -24,8 +25,9 @@
 //                                     column sums, over shared-memory rings
 //   longer rows, unaligned tensors    column sums, then dx
 //
-// Measured, 16384 x 4096 bf16 with fp32 parameters: forward 45 us (5.9 TB/s),
-// backward 75 us (5.4 TB/s) and 4 to 6 more for the join of dgamma and dbeta.
+// Measured back to back, 16384 x 4096 bf16 with fp32 parameters: forward 48 us
+// (5.6 TB/s), backward with the join of dgamma and dbeta 80 (5.0 TB/s), or 74
+// replayed from a graph on the same buffers.
 // What bounds the backward is latency at 16 warps per SM: 170 instructions a
 // warp and 256 elements issue in 57 percent of the cycles; two blocks of 64
 // registers (and two rows between barriers) were slower.
