@@ -348,3 +348,23 @@ def test_norm_tensors_of_more_than_2_31_elements(rows, C):
         eg += (a * b).sum(0, dtype=torch.double)
         eb += b.sum(0, dtype=torch.double)
     assert torch.equal(dg.double(), eg.float().double()) and torch.equal(db.double(), eb)
+
+
+@pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,C", [(2400, 1024), (4200, 1001), (40001, 24), (90001, 27), (600, 5120), (300, 16384), (3, 131073)])
+def test_norm_bad_values_stay_in_their_row_of_a_large_tensor(rows, C, dtype, norm):
+    """Rows beside one another in a block and in its stages; the column sums
+    take the bad values of their own columns only (layer norm's and rms norm's
+    normalised row is bad as a whole, so d gamma is; d beta is not)."""
+    x, dy, gamma, beta = _inputs(rows, C, dtype, "f32", 16)
+    clean = mea.norm_fwd(norm, x, gamma, beta)
+    dxc, _, dbc = mea.norm_bwd(norm, x, dy, gamma, *clean[1:], want_dbeta=True)
+    bad = sorted({1, rows // 2, rows - 1})
+    x[bad[0], 0], x[bad[1], C // 2], x[bad[-1], C - 1] = float("nan"), float("inf"), float("-inf")
+    y, mean, invstd = mea.norm_fwd(norm, x, gamma, beta)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    assert torch.equal(y[keep], clean[0][keep]) and y[bad[0]].isnan().all()
+    dx, _, db = mea.norm_bwd(norm, x, dy, gamma, mean, invstd, want_dbeta=True)
+    assert torch.equal(dx[keep], dxc[keep]) and dx[bad[0]].isnan().all() and torch.equal(db, dbc)
