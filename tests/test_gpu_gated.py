@@ -539,3 +539,22 @@ def test_gated_tensors_of_more_than_2_31_elements():
     zs, hs = mea.matmul_gated_act_fwd("swish", x, wg[-n:], wu[-n:])
     assert z.numel() > 2 ** 31 and torch.equal(h[:, -n:], hs)
     assert torch.equal(z[:, -n:], zs[:, n:]) and torch.equal(z[:, N + 64 - n:N + 64], zs[:, :n])
+
+
+@pytest.mark.parametrize("act,param", [(a, _p(a)) for a in ACTS] + [("swish", 1.0), ("swish", -0.7), ("swish", 0.0), ("swish", 2.0)])
+@pytest.mark.parametrize("M,N,K", [(40, 264, 8), (1040, 264, 8), (1040, 264, 1288)])
+def test_gated_fwd_extreme_gates(act, param, M, N, K):
+    """Gates that one product forms exactly, far out on both sides, through the
+    forward's epilogues.  No sum stands behind them: f's evaluation and one
+    rounding bound h."""
+    far = torch.tensor([0.0, 0.5, 1.0, 5.0, 12.0, 13.5, 20.0, 60.0, 88.0, 100.0, 1e3, 1e6, 1e15, 1e30, 3e38], device="cuda")
+    gates = torch.cat([far, -far, torch.linspace(-14, -0.5, 10, device="cuda")])
+    x = torch.zeros(M, K, dtype=BF, device="cuda")
+    x[:, 0], x[:, 1] = gates.repeat(M // 40).to(BF), 1
+    wg, wu = torch.zeros(N, K, dtype=BF, device="cuda"), torch.zeros(N, K, dtype=BF, device="cuda")
+    wg[:, 0], wu[:, 1] = 1, 0.75
+    z, h = mea.matmul_gated_act_fwd(act, x, wg, wu, param)
+    gate, up, want = ref.gated_fwd(act, x, wg, wu, param)
+    assert torch.equal(z.double(), torch.cat([gate, up], 1))
+    bound = want.abs() * (ref.F_REL + ref.HALF[BF] * (1 + ref.F_REL)) + 2 * ref.TINY
+    ref.assert_within(h, want, bound, "h")
